@@ -17,7 +17,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libbsg.so")
 
 OK, EINVAL, EUNSUPPORTED, EHIP = 0, -1, -2, -3
-F32, BF16 = 0, 1
+F32, BF16, E4M3 = 0, 1, 2
 EPI_NONE, EPI_GELU, EPI_SILU_MUL, EPI_GELU_BWD, EPI_SILU_MUL_BWD = 0, 1, 2, 3, 4
 BLOCK = 128
 MAX_EXPERTS = 1024
@@ -33,7 +33,10 @@ SYMBOLS = ("bsg_max_padded_rows", "bsg_topology_sizes", "bsg_route_workspace_byt
            "bsg_route_backward", "bsg_permute_pad", "bsg_permute_pad_gate_backward",
            "bsg_build_topology", "bsg_route_topology", "bsg_route_permute_topology", "bsg_sdd", "bsg_dsd", "bsg_dsd_workspace_bytes",
            "bsg_dsd_combine_top1", "bsg_dstd",
-           "bsg_unpermute_combine", "bsg_stream_copy", "bsg_status_string", "bsg_last_error")
+           "bsg_unpermute_combine", "bsg_rms_norm", "bsg_rms_norm_backward",
+           "bsg_rms_norm_backward_workspace_bytes", "bsg_grouped_gemm",
+           "bsg_grouped_gemm_workspace_bytes", "bsg_grouped_wgrad", "bsg_grad_norm",
+           "bsg_grad_norm_workspace_bytes", "bsg_grad_clip", "bsg_stream_copy", "bsg_status_string", "bsg_last_error")
 
 
 class BsgError(RuntimeError):
@@ -113,6 +116,29 @@ def lib():
                                vp]
         L.bsg_unpermute_combine.restype = i32
         L.bsg_unpermute_combine.argtypes = [vp, i32, i64, vp, vp, i64, i32, i32, vp, i32, vp]
+        f32 = C.c_float
+        L.bsg_rms_norm.restype = i32
+        L.bsg_rms_norm.argtypes = [vp, i64, vp, i64, vp, f32, i64, i32, i32, vp, i64, vp, i64,
+                                   i32, vp, vp, vp]
+        L.bsg_rms_norm_backward_workspace_bytes.restype = sz
+        L.bsg_rms_norm_backward_workspace_bytes.argtypes = [i64, i32]
+        L.bsg_rms_norm_backward.restype = i32
+        L.bsg_rms_norm_backward.argtypes = [vp, i64, vp, i64, vp, i64, vp, vp, i64, i32, i32, vp,
+                                            i64, vp, vp, sz, vp]
+        L.bsg_grouped_gemm_workspace_bytes.restype = sz
+        L.bsg_grouped_gemm_workspace_bytes.argtypes = [i64, i32, i32, i32, i32]
+        L.bsg_grouped_gemm.restype = i32
+        L.bsg_grouped_gemm.argtypes = [vp, vp, i64, vp, vp, vp, i64, i64, vp, i32, vp, i32, i64,
+                                       i32, i32, i32, vp, vp, i64, i32, vp, i32, vp, sz, vp]
+        L.bsg_grouped_wgrad.restype = i32
+        L.bsg_grouped_wgrad.argtypes = [vp, i64, vp, i64, vp, i32, i64, i32, i32, vp, i64, i64,
+                                        i32, i32, vp]
+        L.bsg_grad_norm_workspace_bytes.restype = sz
+        L.bsg_grad_norm_workspace_bytes.argtypes = []
+        L.bsg_grad_norm.restype = i32
+        L.bsg_grad_norm.argtypes = [vp, vp, vp, i32, vp, vp, sz, vp]
+        L.bsg_grad_clip.restype = i32
+        L.bsg_grad_clip.argtypes = [vp, vp, vp, vp, i32, vp, f32, vp]
         L.bsg_status_string.restype = C.c_char_p
         L.bsg_status_string.argtypes = [i32]
         L.bsg_last_error.restype = C.c_char_p
@@ -319,6 +345,213 @@ def unpermute_combine(yp, dest_row, gate, T, k, d, y):
     _check("unpermute_combine", lib().bsg_unpermute_combine(
         _ptr(yp), dtype_code(yp), _ld(yp), _ptr(dest_row), _ptr(gate), T, k, d, _ptr(y),
         dtype_code(y), _stream()))
+
+
+# ------------------------------------------- norm, ragged products, clipping
+#
+# These take their sizes from the tensors, so what the C call cannot see (that
+# the tensors agree, and lie on the current device) is checked here.
+
+def _need(cond, call, what):
+    if not cond:
+        raise ValueError(f"{call}: {what}")
+
+
+def _on_device(call, *tensors):
+    """Every tensor is on the current GPU, whose current stream the call uses."""
+    dev = torch.cuda.current_device() if torch.cuda.is_available() else -1
+    for t in tensors:
+        _need(t is None or (t.is_cuda and t.get_device() == dev), call,
+              "tensors must be on the current GPU")
+
+
+def _rows(call, name, t, T, d, dtype):
+    _need(t.dim() == 2 and tuple(t.shape) == (T, d) and t.dtype == dtype, call,
+          f"{name} must be a [{T}, {d}] tensor of {dtype}")
+    _need(d <= 1 or T == 0 or t.stride(1) == 1, call, f"{name} must be row-major")
+    return t.stride(0) if T > 1 else max(t.stride(0), d)
+
+
+def _vector(call, name, t, n, dtype):
+    _need(t.dim() == 1 and t.numel() == n and t.dtype == dtype and t.is_contiguous(), call,
+          f"{name} must be a contiguous vector of {n} {dtype}")
+
+
+def _nbytes(t):
+    _need(t is None or t.is_contiguous(), "workspace", "must be contiguous")
+    return 0 if t is None else t.numel() * t.element_size()
+
+
+def rms_norm(x, weight, eps, y, h=None, residual=None, y_scale=None, rstd=None):
+    """y = rms_norm(x + residual) * weight; y in x's type, or in
+    torch.float8_e4m3fn with y_scale [T]; h (with a residual) takes the sum."""
+    c = "rms_norm"
+    _on_device(c, x, weight, y, h, residual, y_scale, rstd)
+    _need(x.dim() == 2, c, "x must be a [T, d] tensor")
+    T, d = x.shape
+    f8 = y.dtype == torch.float8_e4m3fn
+    ldx = _rows(c, "x", x, T, d, x.dtype)
+    ldy = _rows(c, "y", y, T, d, y.dtype if f8 else x.dtype)
+    ldr = _rows(c, "residual", residual, T, d, x.dtype) if residual is not None else 0
+    ldh = _rows(c, "h", h, T, d, x.dtype) if h is not None else 0
+    _vector(c, "weight", weight, d, x.dtype)
+    for name, t in (("y_scale", y_scale), ("rstd", rstd)):
+        if t is not None:
+            _vector(c, name, t, T, torch.float32)
+    _check(c, lib().bsg_rms_norm(_ptr(x), ldx, _ptr(residual), ldr, _ptr(weight), eps, T, d,
+                                 dtype_code(x), _ptr(h), ldh, _ptr(y), ldy,
+                                 E4M3 if f8 else dtype_code(x), _ptr(y_scale), _ptr(rstd),
+                                 _stream()))
+
+
+def rms_norm_backward_workspace_bytes(T: int, d: int) -> int:
+    return int(lib().bsg_rms_norm_backward_workspace_bytes(T, d))
+
+
+def rms_norm_backward(dy, h, weight, rstd, dx, dweight, workspace, dh=None):
+    """dx (of x and of the residual alike) and dweight (fp32) from dy and,
+    when given, the gradient dh that reaches h along the residual stream."""
+    c = "rms_norm_backward"
+    _on_device(c, dy, h, weight, rstd, dx, dweight, workspace, dh)
+    _need(dy.dim() == 2, c, "dy must be a [T, d] tensor")
+    T, d = dy.shape
+    lds = [_rows(c, n, t, T, d, dy.dtype) if t is not None else 0
+           for n, t in (("dy", dy), ("dh", dh), ("h", h), ("dx", dx))]
+    _vector(c, "weight", weight, d, dy.dtype)
+    _vector(c, "rstd", rstd, T, torch.float32)
+    _vector(c, "dweight", dweight, d, torch.float32)
+    _check(c, lib().bsg_rms_norm_backward(_ptr(dy), lds[0], _ptr(dh), lds[1], _ptr(h), lds[2],
+                                          _ptr(weight), _ptr(rstd), T, d, dtype_code(dy),
+                                          _ptr(dx), lds[3], _ptr(dweight), _ptr(workspace),
+                                          _nbytes(workspace), _stream()))
+
+
+def _operand_code(t):
+    return E4M3 if t.dtype == torch.float8_e4m3fn else dtype_code(t)
+
+
+def _matrices(call, name, t, shape, dtype):
+    """(ld, stride) of one matrix an expert, [E, rows, cols] with contiguous rows."""
+    _need(t.dim() == 3 and tuple(t.shape) == tuple(shape) and t.dtype == dtype, call,
+          f"{name} must be a {list(shape)} tensor of {dtype}")
+    _need(t.stride(2) == 1 or shape[2] == 1, call, f"{name} must have contiguous rows")
+    return max(t.stride(1), shape[2]) if shape[1] == 1 else t.stride(1), t.stride(0)
+
+
+def grouped_gemm_workspace_bytes(M: int, K: int, N: int, E: int, epilogue="none") -> int:
+    """Bytes of a workspace that lets grouped_gemm split few-row products (0:
+    it never splits this one)."""
+    epi = EPILOGUES[epilogue] if isinstance(epilogue, str) else int(epilogue)
+    return int(lib().bsg_grouped_gemm_workspace_bytes(M, K, N, E, epi))
+
+
+def grouped_gemm(a, row_offsets, b, c, epilogue="none", trans_b=False, a2=None, b2=None,
+                 a_scale=None, b_scale=None, aux_in=None, aux_out=None, workspace=None):
+    """c[r] = epilogue(a[r] @ b[e]) for the rows r of expert e, row_offsets[e]
+    <= r < row_offsets[e + 1].  b is [E, K, N], or [E, N, K] with trans_b, a
+    view with contiguous rows (the layer's W1 [d, E f]: W1.view(d, E,
+    f).permute(1, 0, 2)); a, b of bf16, fp32 or float8_e4m3fn (with a_scale
+    [M], b_scale [E, N], or [2, E, N] with b2).  c is [M, N]; two-plane
+    arrays (silu_mul's aux_out, silu_mul_bwd's aux_in and c) [2, M, N]."""
+    call = "grouped_gemm"
+    _on_device(call, a, row_offsets, b, c, a2, b2, a_scale, b_scale, aux_in, aux_out, workspace)
+    epi = EPILOGUES[epilogue] if isinstance(epilogue, str) else int(epilogue)
+    _need(a.dim() == 2 and b.dim() == 3 and c.dim() in (2, 3), call,
+          "a is [M, K], b one matrix an expert, c [M, N]")
+    M, K = a.shape
+    E, N = b.shape[0], b.shape[1 if trans_b else 2]
+    lda = _rows(call, "a", a, M, K, a.dtype)
+    ldb, stride = _matrices(call, "b", b, (E, N, K) if trans_b else (E, K, N), a.dtype)
+    _vector(call, "row_offsets", row_offsets, E + 1, torch.int32)
+    if a2 is not None:
+        _need(_rows(call, "a2", a2, M, K, a.dtype) == lda, call, "a2 must be laid out as a")
+    if b2 is not None:
+        _need(_matrices(call, "b2", b2, b.shape, a.dtype) == (ldb, stride), call,
+              "b2 must be laid out as b")
+    if a_scale is not None:
+        _vector(call, "a_scale", a_scale, M, torch.float32)
+    if b_scale is not None:
+        n = (2 if b2 is not None else 1) * E * N
+        _need(b_scale.numel() == n and b_scale.dtype == torch.float32 and b_scale.is_contiguous(),
+              call, f"b_scale must be {n} contiguous fp32 values")
+
+    def planes(name, t, two, ld=None):
+        one = t
+        if two:
+            _need(t.dim() == 3 and t.shape[0] == 2, call, f"{name} must be [2, {M}, {N}]")
+            one = t[0]
+        got = _rows(call, name, one, M, N, c.dtype)
+        _need(ld is None or got == ld, call, f"{name} must be laid out as c")
+        _need(not two or M == 0 or t.stride(0) == M * (got if ld is None else ld), call,
+              f"the second plane of {name} must follow the first")
+        return got
+
+    ldc = planes("c", c, epi == EPI_SILU_MUL_BWD)
+    if aux_in is not None:
+        planes("aux_in", aux_in, epi == EPI_SILU_MUL_BWD, ldc)
+    if aux_out is not None:
+        planes("aux_out", aux_out, epi == EPI_SILU_MUL, ldc)
+    _check(call, lib().bsg_grouped_gemm(
+        _ptr(a), _ptr(a2), lda, _ptr(a_scale), _ptr(b), _ptr(b2), ldb, stride, _ptr(b_scale),
+        int(bool(trans_b)), _ptr(row_offsets), E, M, K, N, epi, _ptr(aux_in), _ptr(c), ldc,
+        dtype_code(c), _ptr(aux_out), _operand_code(a), _ptr(workspace), _nbytes(workspace),
+        _stream()))
+
+
+def grouped_wgrad(a, dmat, row_offsets, c):
+    """c[e] = a[rows of e]^T @ dmat[rows of e]: c is an [E, K, N] view with
+    contiguous rows, of a's type or fp32."""
+    call = "grouped_wgrad"
+    _on_device(call, a, dmat, row_offsets, c)
+    _need(a.dim() == 2 and dmat.dim() == 2 and c.dim() == 3, call,
+          "a is [M, K], dmat [M, N], c one matrix an expert")
+    M, K = a.shape
+    N, E = dmat.shape[1], c.shape[0]
+    lda = _rows(call, "a", a, M, K, a.dtype)
+    ldd = _rows(call, "dmat", dmat, M, N, a.dtype)
+    ldc, stride = _matrices(call, "c", c, (E, K, N), c.dtype)
+    _vector(call, "row_offsets", row_offsets, E + 1, torch.int32)
+    _check(call, lib().bsg_grouped_wgrad(_ptr(a), lda, _ptr(dmat), ldd, _ptr(row_offsets), E, M,
+                                         K, N, _ptr(c), ldc, max(stride, 1), dtype_code(c),
+                                         dtype_code(a), _stream()))
+
+
+def _tensor_list(call, name, tensors):
+    for t in tensors:
+        _need(t.is_contiguous(), call, f"{name} must be contiguous")
+    n = len(tensors)
+    return ((C.c_void_p * n)(*[t.data_ptr() for t in tensors]),
+            (C.c_int64 * n)(*[t.numel() for t in tensors]),
+            (C.c_int * n)(*[dtype_code(t) for t in tensors]))
+
+
+def grad_norm_workspace_bytes() -> int:
+    return int(lib().bsg_grad_norm_workspace_bytes())
+
+
+def grad_norm(grads, norm, workspace):
+    """norm (one fp32) = the 2-norm over all values of the tensors in grads."""
+    c = "grad_norm"
+    _on_device(c, norm, workspace, *grads)
+    _need(norm.numel() == 1 and norm.dtype == torch.float32, c, "norm must be one fp32 value")
+    ptrs, counts, dtypes = _tensor_list(c, "grads", grads)
+    _check(c, lib().bsg_grad_norm(ptrs, counts, dtypes, len(grads), _ptr(norm), _ptr(workspace),
+                                  _nbytes(workspace), _stream()))
+
+
+def grad_clip(grads, norm, max_norm, out=None):
+    """Scale grads by min(1, max_norm / norm), in place or into out."""
+    c = "grad_clip"
+    _on_device(c, norm, *grads, *(out or ()))
+    _need(norm.numel() == 1 and norm.dtype == torch.float32, c, "norm must be one fp32 value")
+    ptrs, counts, dtypes = _tensor_list(c, "grads", grads)
+    to = None
+    if out is not None:
+        _need([(t.numel(), t.dtype) for t in out] == [(t.numel(), t.dtype) for t in grads], c,
+              "out must have the sizes and types of grads")
+        to = _tensor_list(c, "out", out)[0]
+    _check(c, lib().bsg_grad_clip(ptrs, to, counts, dtypes, len(grads), _ptr(norm), max_norm,
+                                  _stream()))
 
 
 def stream_copy(src, dst, nbytes=None):

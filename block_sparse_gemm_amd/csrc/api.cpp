@@ -4,12 +4,11 @@
 #include "../../include/bsg.h"
 
 #include <hip/hip_runtime.h>
-#include <stdarg.h>
-#include <stdio.h>
 
 #include <algorithm>
 #include <mutex>
 
+#include "api.hpp"
 #include "kernels.hpp"
 
 static_assert(bsg::kRouteScratchBytes == BSG_ROUTE_SCRATCH_BYTES, "one scratch size");
@@ -17,47 +16,7 @@ static_assert(bsg::kSplitShareBytes == BSG_DSD_SHARE_BYTES, "one share size");
 
 namespace {
 
-thread_local char g_err[512] = "";
-
-bsg_status fail(bsg_status s, const char* fmt, ...) {
-    va_list ap;
-    va_start(ap, fmt);
-    vsnprintf(g_err, sizeof g_err, fmt, ap);
-    va_end(ap);
-    return s;
-}
-
-bsg_status ok() {
-    g_err[0] = '\0';
-    return BSG_OK;
-}
-
-bsg_status hip_status(hipError_t e, const char* what) {
-    if (e == hipSuccess) return ok();
-    return fail(BSG_EHIP, "%s: %s", what, hipGetErrorString(e));
-}
-
-bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
-
-// Bounds checked before any size is multiplied, so that validation itself
-// never overflows: tokens and block rows fit int32 ids, leading dimensions
-// and widths stay far below the point where a byte count would wrap.
-constexpr int64_t kMaxLd = int64_t(1) << 40;
-constexpr int kMaxWidth = 1 << 24;
-
-int elt_bytes(int dtype) { return dtype == BSG_BF16 ? 2 : 4; }
-
-bool dtype_ok(int dtype) { return dtype == BSG_F32 || dtype == BSG_BF16; }
-
-#define REQUIRE(cond, ...)                                 \
-    do {                                                   \
-        if (!(cond)) return fail(BSG_EINVAL, __VA_ARGS__); \
-    } while (0)
-
-// A device array read or written with 16-byte vectors.
-#define REQUIRE_VEC_PTR(p) REQUIRE((p) != nullptr && aligned((p), 16), #p " must be a non-null 16-byte aligned device pointer")
-// A device array of 4-byte elements.
-#define REQUIRE_PTR(p) REQUIRE((p) != nullptr && aligned((p), 4), #p " must be a non-null 4-byte aligned device pointer")
+using namespace bsg;
 
 bsg_status check_topology(const bsg_topology* t) {
     REQUIRE(t != nullptr, "topo is NULL");
@@ -124,11 +83,11 @@ const char* bsg_status_string(bsg_status s) {
     }
 }
 
-const char* bsg_last_error(void) { return g_err; }
+const char* bsg_last_error(void) { return bsg::g_err; }
 
 int64_t bsg_max_padded_rows(int64_t T, int k, int E, int bin_rows) {
     if (T < 1 || T > INT32_MAX || k < 1 || E < 1 || k > E ||
-        (bin_rows != 64 && bin_rows != 128 && bin_rows != 256))
+        (bin_rows != 1 && bin_rows != 64 && bin_rows != 128 && bin_rows != 256))
         return -1;
     const int64_t A = T * k;
     const int64_t ne = A < E ? A : E;
@@ -159,11 +118,12 @@ size_t bsg_route_workspace_bytes(int64_t T, int k, int E) {
     return (size_t)(nchunks * E * (int64_t)sizeof(int32_t));
 }
 
-// The bin granularity: 128 (the block), or 64 or 256 for the block-size
-// study (bins of 64 rows go with a topology of 64-row blocks).
+// The bin granularity: 128 (the block), 64 or 256 for the block-size study
+// (bins of 64 rows go with a topology of 64-row blocks), or 1 for ragged
+// groups (the grouped products; no topology).
 static bsg_status check_bin(int bin_rows) {
-    REQUIRE(bin_rows == 64 || bin_rows == 128 || bin_rows == 256,
-            "bin_rows must be 64, 128 or 256");
+    REQUIRE(bin_rows == 1 || bin_rows == 64 || bin_rows == 128 || bin_rows == 256,
+            "bin_rows must be 1, 64, 128 or 256");
     return BSG_OK;
 }
 
@@ -421,8 +381,10 @@ bsg_status bsg_route_permute_topology(const float* logits, int64_t T, int E, int
                       "route_permute_topology");
 }
 
+}  // extern "C"
+
 // Compute units of the stream's device, looked up once per device.
-static hipError_t device_cus(hipStream_t stream, int* ncu) {
+hipError_t bsg::device_cus(hipStream_t stream, int* ncu) {
     constexpr int kMaxDevices = 64;
     static std::mutex mu;
     static int cus[kMaxDevices] = {};
@@ -442,6 +404,8 @@ static hipError_t device_cus(hipStream_t stream, int* ncu) {
     *ncu = cus[dev];
     return hipSuccess;
 }
+
+extern "C" {
 
 static bsg::GemmParams gemm_params(const bsg_topology* t) {
     bsg::GemmParams p{};
@@ -506,7 +470,7 @@ bsg_status bsg_sdd(const void* a, int64_t lda, const void* b, const void* b2, in
     p.ldb = ldb;
     p.K = K;
     // the compute units size the split of a sparse last round
-    const hipError_t e = device_cus((hipStream_t)stream, &p.ncu);
+    const hipError_t e = bsg::device_cus((hipStream_t)stream, &p.ncu);
     if (e != hipSuccess) return hip_status(e, "sdd");
     return hip_status(bsg::launch_sdd(p, tiles_max(topo), trans_b,
                                       epilogue, dtype, (hipStream_t)stream),
@@ -516,7 +480,7 @@ bsg_status bsg_sdd(const void* a, int64_t lda, const void* b, const void* b2, in
 bsg_status bsg_dsd_workspace_bytes(bsg_stream_t stream, int64_t* bytes) {
     REQUIRE(bytes != nullptr, "bytes is NULL");
     int ncu = 0;
-    const hipError_t e = device_cus((hipStream_t)stream, &ncu);
+    const hipError_t e = bsg::device_cus((hipStream_t)stream, &ncu);
     if (e != hipSuccess) return hip_status(e, "dsd_workspace_bytes");
     *bytes = (int64_t)ncu * bsg::kSplitShareBytes;
     return ok();
@@ -569,7 +533,7 @@ bsg_status bsg_dsd(const void* blocks, const void* blocks2, const bsg_topology* 
     // the last round's split: only tiles of at least kSplitMinBlocks K-blocks
     if (workspace && (int64_t)topo->F * (blocks2 ? 2 : 1) >= bsg::kSplitMinBlocks) {
         int ncu = 0;
-        const hipError_t e = device_cus((hipStream_t)stream, &ncu);
+        const hipError_t e = bsg::device_cus((hipStream_t)stream, &ncu);
         if (e != hipSuccess) return hip_status(e, "dsd");
         p.ws = (float*)workspace;
         p.ws_units = (int)std::min<size_t>(workspace_bytes / bsg::kSplitShareBytes, INT32_MAX);

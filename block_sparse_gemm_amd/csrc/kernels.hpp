@@ -8,6 +8,7 @@ namespace bsg {
 
 constexpr int kF32 = 0;   // matches BSG_F32
 constexpr int kBf16 = 1;  // matches BSG_BF16
+constexpr int kE4m3 = 2;  // matches BSG_E4M3
 
 constexpr int kEpiNone = 0;
 constexpr int kEpiGelu = 1;
@@ -151,6 +152,74 @@ hipError_t launch_dstd(const GemmParams& p, int trans_c, int dtype, hipStream_t 
 hipError_t launch_unpermute_combine(const void* yp, int yp_dtype, int64_t ld_yp,
                                     const int32_t* dest_row, const float* gate, int64_t T, int k,
                                     int d, void* y, int y_dtype, hipStream_t stream);
+
+// Ragged grouped products (launch_grouped_wgrad's meaning in brackets).
+// Leading dimensions and strides in elements.
+struct GroupedParams {
+    const void* a;         // [M, K]                        [A, M x K]
+    const void* a2;        // second set of a two-set product, or NULL
+    const void* b;         // [E] matrices of B             [D, M x N]
+    const void* b2;        // SILU_MUL: up projection; two sets: the second's B
+    const void* aux_in;
+    const float* a_scale;  // e4m3: [M]
+    const float* b_scale;  // e4m3: [E, N], with b2 [2, E, N]
+    const int32_t* row_offsets;  // [E + 1]
+    void* c;               // [M, N] (SILU_MUL_BWD: two planes)  [[E] K x N]
+    void* aux_out;
+    float* ws;             // partial sums of the few-row kernel, or NULL
+    int64_t ws_floats;
+    int64_t lda, ldb, ldc;
+    int64_t stride_b;      // from an expert's matrix to the next one's  [of c]
+    int64_t M;
+    int K, N, E;
+    int ncu;
+};
+
+hipError_t launch_grouped_gemm(const GroupedParams& p, int trans_b, int epi, int c_dtype, int dtype,
+                               hipStream_t stream);
+hipError_t launch_grouped_wgrad(const GroupedParams& p, int c_dtype, int dtype, hipStream_t stream);
+// the tile kernel, by operand type (grouped_bf16.hip, grouped_f32.hip, grouped_e4m3.hip)
+hipError_t launch_grouped_bf16(const GroupedParams& p, int trans_b, int epi, int c_dtype,
+                               hipStream_t stream);
+hipError_t launch_grouped_f32(const GroupedParams& p, int trans_b, int epi, hipStream_t stream);
+hipError_t launch_grouped_e4m3(const GroupedParams& p, int epi, hipStream_t stream);
+
+// What the norm's kernels read and write (launch_rms_norm_backward's names
+// in brackets).  Leading dimensions in elements of the array's own type.
+struct NormParams {
+    const void* x;         // [T, d]                       [h]
+    const void* residual;  // [T, d] or NULL               [dh or NULL]
+    const void* dy;        //                              [dy]
+    const void* weight;    // [d]
+    void* h;               // [T, d] or NULL: rd(x + r)
+    void* y;               // [T, d]                       [dx]
+    float* y_scale;        // [T], e4m3 output
+    float* rstd;           // [T] or NULL, written         [read]
+    float* partial;        //                              [workspace: rows of partial dw]
+    int64_t ldx, ldr, ldh, ldy;  //                        [h, dh, dx, dy]
+    int64_t T;
+    int d;
+    float eps;
+};
+
+constexpr int kNormRowBytes = 32768;  // widest row
+constexpr int kNormPartials = 512;    // most partial rows of dw
+
+int rms_norm_backward_rows(int64_t T, int d, int dtype);  // partial rows of dw
+
+hipError_t launch_rms_norm(const NormParams& p, int dtype, int q8, hipStream_t stream);
+hipError_t launch_rms_norm_backward(const NormParams& p, int dtype, float* dweight,
+                                    hipStream_t stream);
+
+// The partial sums of squares of a list of gradients: at most this many
+// workgroups, one fp64 partial sum each.
+constexpr int kClipBlocks = 2048;
+
+hipError_t launch_grad_norm(const void* const* grads, const int64_t* counts, const int* dtypes,
+                            int n, float* norm, double* partial, hipStream_t stream);
+hipError_t launch_grad_clip(const void* const* grads, void* const* out, const int64_t* counts,
+                            const int* dtypes, int n, const float* norm, float max_norm,
+                            hipStream_t stream);
 
 hipError_t launch_stream_copy(const void* src, void* dst, int64_t words, hipStream_t stream);
 
