@@ -127,11 +127,12 @@ bsg_status bsg_rms_norm_backward(const void* dy, int64_t lddy, const void* dh, i
 
 // ------------------------------------------------------- grouped products
 
-// The grouped products' lane offsets inside a panel stay below 2^31, which
-// leaves the bit that puts a lane out of its panel's range.
+// The grouped products' lane offsets inside an operand's 256 rows (K
+// contiguous) or K-tile stay below 2^31, which leaves the bit that puts a
+// lane out of its operand's range; so does a row, the scalar offset's range.
 static bool grouped_ld_fits(int64_t ld, int es, bool k_contiguous) {
-    const int64_t last_row = k_contiguous ? 127 : (es == 2 ? 31 : 15);
-    const int64_t row_bytes = k_contiguous ? 64 : 256 * (es == 2 ? 1 : 2);
+    const int64_t last_row = k_contiguous ? 255 : (es == 2 ? 31 : 15);
+    const int64_t row_bytes = k_contiguous ? 64 + (int64_t)kMaxWidth * es : 512 * es;
     return last_row * ld * es + row_bytes <= (int64_t)INT32_MAX;
 }
 
@@ -139,7 +140,7 @@ static bool grouped_ld_fits(int64_t ld, int es, bool k_contiguous) {
     do {                                                                                   \
         if (!grouped_ld_fits((ld), (es), (kc)))                                            \
             return fail(BSG_EUNSUPPORTED, #ld " = %lld is too large for the products' "    \
-                        "31-bit panel offsets", (long long)(ld));                          \
+                        "31-bit offsets", (long long)(ld));                          \
     } while (0)
 
 static int grouped_elt_bytes(int dtype) { return dtype == BSG_E4M3 ? 1 : elt_bytes(dtype); }

@@ -121,54 +121,54 @@ __device__ __forceinline__ Group group_of(const int32_t* __restrict__ off, int E
     return g;
 }
 
-// -------------------------------------------------------------- panels
+// -------------------------------------------------------------- operands
 
-// A panel's place in memory, K-tile after K-tile: `left` bytes from `base`
-// to the end of its data, `step` bytes to the next K-tile.
-struct Panel {
+// One operand of a tile in memory: 256 rows (or columns) as two panels of
+// 128, K-tile after K-tile.  `left` bytes from `base` to the end of its data.
+struct Operand {
     const char* base;
-    int64_t left, step;
+    int64_t left;
 };
 
-// K contiguous: `rows` rows (0 for none) of K_b bytes.
-__device__ __forceinline__ Panel panel_k(const void* p, int64_t first, int64_t ld_b, int rows,
-                                         int64_t K_b) {
-    rows = min(max(rows, 0), 128);
-    return Panel{(const char*)p + first * ld_b, rows > 0 ? (int64_t)(rows - 1) * ld_b + K_b : 0, kRowBytes};
+// K contiguous: rows [first, first + rows) (256 at most are read) of K_b bytes.
+__device__ __forceinline__ Operand operand_k(const void* p, int64_t first, int64_t ld_b, int64_t rows,
+                                             int64_t K_b) {
+    rows = rows < 256 ? rows : 256;
+    return Operand{(const char*)p + first * ld_b, (rows - 1) * ld_b + K_b};
 }
 
-// M or N contiguous: k rows of `width_b` bytes from column byte `col_b` on.
-__device__ __forceinline__ Panel panel_n(const void* p, int64_t ld_b, int64_t col_b, int64_t width_b,
-                                         int64_t k, int kt) {
-    const int64_t w = width_b - col_b;
-    return Panel{(const char*)p + col_b, w > 0 && k > 0 ? (k - 1) * ld_b + w : 0, kt * ld_b};
+// M or N contiguous: k rows of `width_b` bytes, from column byte `col_b` on.
+__device__ __forceinline__ Operand operand_n(const void* p, int64_t ld_b, int64_t col_b,
+                                             int64_t width_b, int64_t k) {
+    return Operand{(const char*)p + col_b, (k - 1) * ld_b + width_b - col_b};
 }
 
-// The buffer descriptor of what is left of a panel.  Raw buffer, offsets in
-// bytes; the lane offsets stay below 2^31 (checked on the host), so a range
-// capped there cuts nothing off and bit 31 puts a lane out of range.
-__device__ __forceinline__ u32x4 descriptor(const Panel& p) {
-    const uint64_t a = (uint64_t)p.base;
-    const int64_t n = p.left < 0 ? 0 : p.left > 0x7fffffff ? 0x7fffffff : p.left;
+// The buffer descriptor of `left` bytes from `base`: raw, offsets in bytes.
+// The lane offsets stay below 2^31 (checked on the host), so a range capped
+// there cuts nothing off and bit 31 puts a lane out of range.
+__device__ __forceinline__ u32x4 descriptor(const char* base, int64_t left) {
+    const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)left);
+    const int hi = __builtin_amdgcn_readfirstlane((int)(left >> 32));
     u32x4 d;
-    d[0] = __builtin_amdgcn_readfirstlane((uint32_t)a);
-    d[1] = __builtin_amdgcn_readfirstlane((uint32_t)(a >> 32) & 0xffffu);
-    d[2] = __builtin_amdgcn_readfirstlane((uint32_t)n);
+    d[0] = __builtin_amdgcn_readfirstlane((uint32_t)(uint64_t)base);
+    d[1] = __builtin_amdgcn_readfirstlane((uint32_t)((uint64_t)base >> 32) & 0xffffu);
+    d[2] = hi < 0 ? 0u : hi > 0 || lo > 0x7fffffffu ? 0x7fffffffu : lo;
     d[3] = 0x00020000u;
     return d;
 }
 
-// 16 bytes a lane from memory to LDS byte lds_addr + 16 lane; zeros for
+// 16 bytes a lane from memory to LDS byte lds_addr + OFF + 16 lane; zeros for
 // lanes out of the descriptor's range.  Inline asm for the reason given at
 // dma16: the kernel itself waits for these loads before the barrier that
 // publishes their stage.  The s_nop covers the five wait states a descriptor
 // register needs when a vector instruction (a spilled register's restore)
 // wrote it just before.
-__device__ __forceinline__ void dma16_range(uint32_t lds_addr, u32x4 desc, uint32_t off) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+template <int OFF>
+__device__ __forceinline__ void dma16_range(uint32_t lds_addr, u32x4 desc, uint32_t off, uint32_t soff) {
+    asm volatile("s_add_u32 m0, %0, %4\n\ts_nop 3\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
                  :
-                 : "s"(__builtin_amdgcn_readfirstlane(lds_addr)), "v"(off), "s"(desc)
-                 : "memory");
+                 : "s"(lds_addr), "v"(off), "s"(desc), "s"(soff), "n"(OFF)
+                 : "memory", "scc");
 }
 
 typedef int i32x8 __attribute__((ext_vector_type(8)));
@@ -184,16 +184,24 @@ __device__ __forceinline__ void mma_stage(f32x16& acc, const u32x4* x, const u32
             a[i] = (int)x[0][i], a[4 + i] = (int)x[1][i];
             b[i] = (int)y[0][i], b[4 + i] = (int)y[1][i];
         }
-        // block scales of 2^0 (127 in e8m0).  The instruction adds the products
+        // no block scales (zero operands select the plain instruction).  It adds the products
         // of 8 neighbouring k with 13 bits below the largest one (measured: next
         // to a product of 1, products of 2^-13 count and of 2^-14 do not), then
         // goes on in fp32.  The rate is twice bf16's, and 7 * 2^-13 of the sum
         // of sizes is far below what rounding the operands to e4m3 cost.
-        acc = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, acc, 0, 0, 0, 0x7f7f7f7f, 0,
-                                                              0x7f7f7f7f);
+        acc = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, acc, 0, 0, 0, 0, 0, 0);
     } else {
         mma<DT>(acc, x[0], y[0]);
         mma<DT>(acc, x[1], y[1]);
+    }
+}
+
+// f(0), ..., f(N - 1) with the index as a constant.
+template <int N, typename F, int I = 0>
+__device__ __forceinline__ void unroll(F&& f) {
+    if constexpr (I < N) {
+        f(std::integral_constant<int, I>{});
+        unroll<N, F, I + 1>(static_cast<F&&>(f));
     }
 }
 
@@ -216,12 +224,12 @@ struct TileOut {
 };
 
 // AK, BK: operand K-contiguous.  HALF: at most 128 rows (waves split them 64
-// by 64 and the second A panel is not loaded).  Kb: bytes of K of one set;
-// sets 2: a second pair of operands (second[]) into the same accumulators.
+// by 64 and the second A panel is not loaded).  K of one set; sets 2: a second
+// pair of operands into the same accumulators.  op: A, B (DUAL: its second
+// panel's B) of the first set, then of the second.
 template <int DT, bool AK, bool BK, int EPI, int OUT, bool HALF>
-__device__ __forceinline__ void ragged_tile(char* smem, const Panel* first, const Panel* second,
-                                             int64_t lda_b, int64_t ldb_b, int64_t K, int sets,
-                                             const TileOut& o) {
+__device__ __forceinline__ void ragged_tile(char* smem, const Operand (*op)[3], int64_t lda_b,
+                                             int64_t ldb_b, int64_t K, int sets, const TileOut& o) {
     constexpr int ES = GElt<DT>::kBytes, KT = GElt<DT>::kKt;
     constexpr bool DUAL = EPI == kEpiSiluMul || EPI == kEpiSiluMulSave;
     constexpr int LPT = HALF ? kLoadsPerTile - 2 : kLoadsPerTile;
@@ -230,53 +238,80 @@ __device__ __forceinline__ void ragged_tile(char* smem, const Panel* first, cons
     lds_t* lds = (lds_t*)smem;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wave & 1, wn = wave >> 1, l32 = lane & 31, lh = lane >> 5;
+    // the layouts follow the operand's bytes: e4m3 is K-contiguous, where the
+    // type does not matter
+    constexpr int LT = DT == kE4m3 ? kBf16 : DT;
 
     const int nk1 = (int)((K + KT - 1) / KT), nk = nk1 * sets;
-    // bytes of K in the last K-tile of a set
-    const int last_b = (int)(K - (int64_t)(nk1 - 1) * KT) * ES;
-    uint32_t aoff[kSegsPerWave], boff[kSegsPerWave], atail[kSegsPerWave], btail[kSegsPerWave];
+
+    // ---- loads: K-tile `lt` is next to go out.  Panels 0, 1: A; 2, 3: B.
+    // The second panel of an operand is the first one's descriptor with
+    // larger lane offsets.  K-contiguous operands advance through the scalar
+    // offset under a constant descriptor; the others move their base.
+    constexpr int NOP = DUAL ? 3 : 2;
+    uint32_t off[4][kSegsPerWave];
 #pragma unroll
     for (int j = 0; j < kSegsPerWave; ++j) {
         const int s = wave * kSegsPerWave + j;
-        // the layouts follow the operand's bytes: e4m3 is K-contiguous, where
-        // the type does not matter
-        constexpr int LT = DT == kE4m3 ? kBf16 : DT;
-        aoff[j] = (uint32_t)seg_offset<LT, AK>(s, lane, lda_b);
-        boff[j] = (uint32_t)seg_offset<LT, BK>(s, lane, ldb_b);
-        const int row = s * 16 + (lane >> 2);
-        const bool behind = ((lane & 3) ^ ((row >> 2) & 3)) * 16 >= last_b;
-        atail[j] = AK && behind ? aoff[j] | 0x80000000u : aoff[j];
-        btail[j] = BK && behind ? boff[j] | 0x80000000u : boff[j];
+        const uint32_t fa = (uint32_t)seg_offset<LT, AK>(s, lane, lda_b);
+        const uint32_t fb = (uint32_t)seg_offset<LT, BK>(s, lane, ldb_b);
+        off[0][j] = fa;
+        off[1][j] = fa + (uint32_t)(AK ? 128 * lda_b : 128 * ES);
+        off[2][j] = fb;
+        off[3][j] = DUAL ? fb : fb + (uint32_t)(BK ? 128 * ldb_b : 128 * ES);
     }
-
-    // ---- loads: K-tile `lt` is next to go out
-    Panel pan[4];
+    // lanes whose 16 bytes lie behind K in a set's last K-tile (K contiguous;
+    // the chunk a lane fetches does not depend on its segment)
+    const int last_b = (int)(K - (int64_t)(nk1 - 1) * KT) * ES;
+    const uint32_t behind = ((lane & 3) ^ ((lane >> 4) & 3)) * 16 >= last_b ? 0x80000000u : 0u;
+    constexpr bool TWO = EPI == kEpiNone;  // may take a second set
+    const char* base[NOP];
+    int64_t left[NOP];
+    u32x4 desc[NOP], desc2[NOP];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) pan[i] = first[i];
-    u32x4 desc[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) desc[i] = descriptor(pan[i]);
+    for (int i = 0; i < NOP; ++i) {
+        base[i] = op[0][i].base;
+        left[i] = op[0][i].left;
+        desc[i] = descriptor(base[i], left[i]);
+        desc2[i] = descriptor(op[1][i].base, op[1][i].left);
+    }
     int lt = 0;
+    uint32_t soff = 0;                        // bytes of K behind the K-contiguous operands
+    uint32_t tail = nk1 == 1 ? behind : 0u;   // `behind` while K-tile lt is a set's last
     const uint32_t lds0 = lds_u32(lds) + wave * kSegsPerWave * 1024;
-    auto dma = [&](int j) {  // load j (0..7): panel j & 3, segment j >> 2
-        const int pnl = j & 3, sg = j >> 2;
-        if (HALF && pnl == 1) return;
-        const bool tail = lt == nk1 - 1 || lt == nk - 1;
-        const uint32_t off = pnl < 2 ? (tail ? atail[sg] : aoff[sg]) : (tail ? btail[sg] : boff[sg]);
-        dma16_range(lds0 + (lt % kStages) * kStageBytes + pnl * kPanelBytes + sg * 1024, desc[pnl], off);
+    uint32_t lds_lt = lds0;                   // this wave's segments in K-tile lt's stage
+    auto dma = [&](auto jc) {  // load j (0..7): panel j & 3, segment j >> 2
+        constexpr int j = decltype(jc)::value, pnl = j & 3, sg = j >> 2;
+        constexpr int i = pnl < 2 ? 0 : DUAL && pnl == 3 ? 2 : 1;
+        constexpr bool KC = i == 0 ? AK : BK;
+        if constexpr (HALF && pnl == 1) return;
+        else
+            dma16_range<pnl * kPanelBytes + sg * 1024>(
+                lds_lt, desc[i], KC ? off[pnl][sg] | tail : off[pnl][sg], KC ? soff : 0u);
     };
+    // Selects, not branches: behind a branch the compiler gathers the MFMAs
+    // that should run among the loads.
     auto next = [&]() {
         ++lt;
-        const bool swap = lt == nk1 && sets == 2, past = lt >= nk;
+        lds_lt = lds0 + (lt % kStages) * kStageBytes;
+        const bool over = lt >= nk, swap = TWO && lt == nk1;
+        soff = over || swap ? 0u : soff + kRowBytes;
+        tail = lt == nk1 - 1 || lt == nk - 1 ? behind : 0u;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if (swap) {
-                pan[i] = second[i];
+        for (int i = 0; i < NOP; ++i) {
+            if (i == 0 ? AK : BK) {
+                if constexpr (TWO) {
+                    desc[i][0] = swap ? desc2[i][0] : desc[i][0];
+                    desc[i][1] = swap ? desc2[i][1] : desc[i][1];
+                    desc[i][2] = swap ? desc2[i][2] : desc[i][2];
+                }
+                desc[i][2] = over ? 0u : desc[i][2];
             } else {
-                pan[i].base += pan[i].step;
-                pan[i].left = past ? 0 : pan[i].left - pan[i].step;
+                const int64_t step = KT * (i == 0 ? lda_b : ldb_b);
+                base[i] = swap ? op[1][i].base : base[i] + step;
+                left[i] = swap ? op[1][i].left : left[i] - step;
+                desc[i] = descriptor(base[i], over ? 0 : left[i]);
             }
-            desc[i] = descriptor(pan[i]);
         }
     };
 
@@ -288,7 +323,6 @@ __device__ __forceinline__ void ragged_tile(char* smem, const Panel* first, cons
 #pragma unroll
             for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
 
-    constexpr int LT = DT == kE4m3 ? kBf16 : DT;
     // fragment f (0..NMI-1: A, then four of B), K piece c of K-tile t
     auto read1 = [&](int t, int c, int f, u32x4 (*af)[2], u32x4 (*bf)[2]) {
         const lds_t* st = lds + (t % kStages) * kStageBytes;
@@ -311,31 +345,26 @@ __device__ __forceinline__ void ragged_tile(char* smem, const Panel* first, cons
     // an odd number of K-tiles ends with one of zeros.
     auto step = [&](int t, auto cur) {
         constexpr int c0 = decltype(cur)::value, c1 = 1 - c0;
-        constexpr int NF = NMI + 4, GROUPS = NMI * 2;
+        // fragment reads, MFMA groups, and the groups the reads are spread over:
+        // the last ones have no reads, so the next barrier finds them returned
+        constexpr int NR = 2 * (NMI + 4), GROUPS = NMI * 4, READ = GROUPS * 3 / 4;
         wait_tiles<LPT>(kStages - 2);
         __syncthreads();
+        unroll<GROUPS>([&](auto gc) {
+            constexpr int g = decltype(gc)::value;
 #pragma unroll
-        for (int g = 0; g < GROUPS; ++g) {
-#pragma unroll
-            for (int f = g * NF / GROUPS; f < (g + 1) * NF / GROUPS; ++f) {
-                read1(t + 1, 0, f, af[c1], bf[c1]);
-                read1(t + 1, 1, f, af[c1], bf[c1]);
-            }
-#pragma unroll
-            for (int j = g * 8 / GROUPS; j < (g + 1) * 8 / GROUPS; ++j) dma(j);
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int mi = (2 * g + h) >> 2, ni = (2 * g + h) & 3;
-                mma_stage<DT>(acc[mi][ni], bf[c0][ni], af[c0][mi]);
-            }
+            for (int r = g * NR / READ; r < (g + 1) * NR / READ && r < NR; ++r)
+                read1(t + 1, r & 1, r >> 1, af[c1], bf[c1]);
+            if constexpr (HALF) dma(gc);
+            else if constexpr (g % 2 == 0) dma(std::integral_constant<int, g / 2>{});
+            if constexpr (g == GROUPS - 1) next();
+            mma_stage<DT>(acc[g >> 2][g & 3], bf[c0][g & 3], af[c0][g >> 2]);
             __builtin_amdgcn_sched_barrier(0);
-        }
-        next();
+        });
     };
     if (nk > 0) {
         for (int t = 0; t < kStages; ++t) {
-#pragma unroll
-            for (int j = 0; j < kLoadsPerTile; ++j) dma(j);
+            unroll<kLoadsPerTile>(dma);
             next();
         }
         wait_tiles<LPT>(kStages - 1);
@@ -499,20 +528,13 @@ __global__ __launch_bounds__(kGemmThreads, 1) void grouped_gemm_kernel(GroupedPa
     const int64_t row = (int64_t)g.row0 + 256 * tm;
     const int n0 = tq * W;
     const int64_t lda_b = P.lda * ES, ldb_b = P.ldb * ES, K_b = (int64_t)P.K * ES;
-    Panel pan[2][4];
-#pragma unroll
-    for (int s = 0; s < 2; ++s) {
-        const void* A = s ? P.a2 : P.a;
-        pan[s][0] = panel_k(A, row, lda_b, mr, K_b);
-        pan[s][1] = panel_k(A, row + 128, lda_b, mr - 128, K_b);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const char* B = (const char*)(s || (DUAL && i) ? P.b2 : P.b) + (int64_t)g.e * P.stride_b * ES;
-            const int c = DUAL ? n0 : n0 + 128 * i;
-            if constexpr (BK) pan[s][2 + i] = panel_k(B, c, ldb_b, P.N - c, K_b);
-            else pan[s][2 + i] = panel_n(B, ldb_b, (int64_t)c * ES, (int64_t)P.N * ES, P.K, KT);
-        }
-    }
+    const int64_t eb = (int64_t)g.e * P.stride_b * ES;
+    auto B = [&](const void* b) {
+        if constexpr (BK) return operand_k((const char*)b + eb, n0, ldb_b, P.N - n0, K_b);
+        else return operand_n((const char*)b + eb, ldb_b, (int64_t)n0 * ES, (int64_t)P.N * ES, P.K);
+    };
+    const Operand op[2][3] = {{operand_k(P.a, row, lda_b, mr, K_b), B(P.b), B(P.b2)},
+                              {operand_k(P.a2, row, lda_b, mr, K_b), B(P.b2), B(P.b2)}};
     TileOut o{};
     o.ldc = P.ldc;
     o.mr = mr;
@@ -532,9 +554,9 @@ __global__ __launch_bounds__(kGemmThreads, 1) void grouped_gemm_kernel(GroupedPa
     }
     const int sets = EPI == kEpiNone && P.a2 ? 2 : 1;
     if (mr <= 128)
-        ragged_tile<DT, true, BK, EPI, OUT, true>(smem, pan[0], pan[1], lda_b, ldb_b, P.K, sets, o);
+        ragged_tile<DT, true, BK, EPI, OUT, true>(smem, op, lda_b, ldb_b, P.K, sets, o);
     else
-        ragged_tile<DT, true, BK, EPI, OUT, false>(smem, pan[0], pan[1], lda_b, ldb_b, P.K, sets, o);
+        ragged_tile<DT, true, BK, EPI, OUT, false>(smem, op, lda_b, ldb_b, P.K, sets, o);
 }
 
 // Weight gradients: C_e [K x N], the reduction along the group's rows; both
@@ -558,12 +580,9 @@ __global__ __launch_bounds__(kGemmThreads, 1) void grouped_wgrad_kernel(GroupedP
     const int64_t lda_b = P.lda * ES, ldb_b = P.ldb * ES;
     const char* A = (const char*)P.a + (int64_t)row0 * lda_b;
     const char* D = (const char*)P.b + (int64_t)row0 * ldb_b;
-    Panel pan[4];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        pan[i] = panel_n(A, lda_b, ((int64_t)tm * 256 + 128 * i) * ES, (int64_t)P.K * ES, rows, KT);
-        pan[2 + i] = panel_n(D, ldb_b, ((int64_t)tq * 256 + 128 * i) * ES, (int64_t)P.N * ES, rows, KT);
-    }
+    const Operand oa = operand_n(A, lda_b, (int64_t)tm * 256 * ES, (int64_t)P.K * ES, rows);
+    const Operand ob = operand_n(D, ldb_b, (int64_t)tq * 256 * ES, (int64_t)P.N * ES, rows);
+    const Operand op[2][3] = {{oa, ob, ob}, {oa, ob, ob}};
     TileOut o{};
     o.ldc = P.ldc;
     o.mr = min(256, P.K - 256 * tm);
@@ -571,9 +590,9 @@ __global__ __launch_bounds__(kGemmThreads, 1) void grouped_wgrad_kernel(GroupedP
     o.N = P.N;
     o.out = (char*)P.c + ((int64_t)e * P.stride_b + (int64_t)tm * 256 * P.ldc) * OES;
     if (o.mr <= 128)
-        ragged_tile<DT, false, false, kEpiNone, OUT, true>(smem, pan, pan, lda_b, ldb_b, rows, 1, o);
+        ragged_tile<DT, false, false, kEpiNone, OUT, true>(smem, op, lda_b, ldb_b, rows, 1, o);
     else
-        ragged_tile<DT, false, false, kEpiNone, OUT, false>(smem, pan, pan, lda_b, ldb_b, rows, 1, o);
+        ragged_tile<DT, false, false, kEpiNone, OUT, false>(smem, op, lda_b, ldb_b, rows, 1, o);
 }
 
 // Most tiles of M rows in E groups, `per` tiles a row tile of H rows: every
