@@ -8,6 +8,7 @@ is missing this module raises on first use.
 """
 from __future__ import annotations
 
+import array
 import ctypes as C
 import os
 
@@ -350,58 +351,77 @@ def unpermute_combine(yp, dest_row, gate, T, k, d, y):
 # ------------------------------------------- norm, ragged products, clipping
 #
 # These take their sizes from the tensors, so what the C call cannot see (that
-# the tensors agree, and lie on the current device) is checked here.
+# the tensors agree, and lie on the current device) is checked here.  The
+# checks are written to cost little: a small call takes about as long here as
+# on the GPU.
 
-def _need(cond, call, what):
-    if not cond:
-        raise ValueError(f"{call}: {what}")
-
-
-def _on_device(call, *tensors):
-    """Every tensor is on the current GPU, whose current stream the call uses."""
-    dev = torch.cuda.current_device() if torch.cuda.is_available() else -1
-    for t in tensors:
-        _need(t is None or (t.is_cuda and t.get_device() == dev), call,
-              "tensors must be on the current GPU")
+_F8 = torch.float8_e4m3fn
+_CODES = {torch.float32: F32, torch.bfloat16: BF16, _F8: E4M3}
 
 
-def _rows(call, name, t, T, d, dtype):
-    _need(t.dim() == 2 and tuple(t.shape) == (T, d) and t.dtype == dtype, call,
-          f"{name} must be a [{T}, {d}] tensor of {dtype}")
-    _need(d <= 1 or T == 0 or t.stride(1) == 1, call, f"{name} must be row-major")
-    return t.stride(0) if T > 1 else max(t.stride(0), d)
+def _fail(call, what):
+    raise ValueError(f"{call}: {what}")
+
+
+def _current(call, tensors):
+    """The current stream, if every tensor (or None) is on the current GPU."""
+    devices = {t.get_device() for t in tensors if t is not None}
+    dev = devices.pop()
+    if devices or dev < 0 or dev != torch.cuda.current_device():
+        _fail(call, "tensors must be on the current GPU")
+    return torch._C._cuda_getCurrentRawStream(dev)
+
+
+def _address(t):
+    return None if t is None else t.data_ptr()
+
+
+def _rows(call, name, t, shape, dtype):
+    """The leading dimension of a row-major [T, d] tensor."""
+    if t.shape != shape or t.dtype != dtype:
+        _fail(call, f"{name} must be a {list(shape)} tensor of {dtype}")
+    ld, one = t.stride()
+    if one != 1 and shape[1] > 1 and shape[0]:
+        _fail(call, f"{name} must be row-major")
+    return ld if shape[0] > 1 or ld > shape[1] else shape[1]
 
 
 def _vector(call, name, t, n, dtype):
-    _need(t.dim() == 1 and t.numel() == n and t.dtype == dtype and t.is_contiguous(), call,
-          f"{name} must be a contiguous vector of {n} {dtype}")
+    if t.dim() != 1 or t.numel() != n or t.dtype != dtype or not t.is_contiguous():
+        _fail(call, f"{name} must be a contiguous vector of {n} {dtype}")
 
 
-def _nbytes(t):
-    _need(t is None or t.is_contiguous(), "workspace", "must be contiguous")
-    return 0 if t is None else t.numel() * t.element_size()
+def _nbytes(call, t):
+    if t is None:
+        return 0
+    if not t.is_contiguous():
+        _fail(call, "the workspace must be contiguous")
+    return t.numel() * t.element_size()
 
 
 def rms_norm(x, weight, eps, y, h=None, residual=None, y_scale=None, rstd=None):
     """y = rms_norm(x + residual) * weight; y in x's type, or in
     torch.float8_e4m3fn with y_scale [T]; h (with a residual) takes the sum."""
     c = "rms_norm"
-    _on_device(c, x, weight, y, h, residual, y_scale, rstd)
-    _need(x.dim() == 2, c, "x must be a [T, d] tensor")
-    T, d = x.shape
-    f8 = y.dtype == torch.float8_e4m3fn
-    ldx = _rows(c, "x", x, T, d, x.dtype)
-    ldy = _rows(c, "y", y, T, d, y.dtype if f8 else x.dtype)
-    ldr = _rows(c, "residual", residual, T, d, x.dtype) if residual is not None else 0
-    ldh = _rows(c, "h", h, T, d, x.dtype) if h is not None else 0
-    _vector(c, "weight", weight, d, x.dtype)
-    for name, t in (("y_scale", y_scale), ("rstd", rstd)):
-        if t is not None:
-            _vector(c, name, t, T, torch.float32)
-    _check(c, lib().bsg_rms_norm(_ptr(x), ldx, _ptr(residual), ldr, _ptr(weight), eps, T, d,
-                                 dtype_code(x), _ptr(h), ldh, _ptr(y), ldy,
-                                 E4M3 if f8 else dtype_code(x), _ptr(y_scale), _ptr(rstd),
-                                 _stream()))
+    stream = _current(c, (x, weight, y, h, residual, y_scale, rstd))
+    shape, dt = x.shape, x.dtype
+    if len(shape) != 2:
+        _fail(c, "x must be a [T, d] tensor")
+    T, d = shape
+    code = dtype_code(x)
+    ycode = E4M3 if y.dtype == _F8 else code
+    ldx = _rows(c, "x", x, shape, dt)
+    ldy = _rows(c, "y", y, shape, _F8 if ycode == E4M3 else dt)
+    ldr = _rows(c, "residual", residual, shape, dt) if residual is not None else 0
+    ldh = _rows(c, "h", h, shape, dt) if h is not None else 0
+    _vector(c, "weight", weight, d, dt)
+    if y_scale is not None:
+        _vector(c, "y_scale", y_scale, T, torch.float32)
+    if rstd is not None:
+        _vector(c, "rstd", rstd, T, torch.float32)
+    _check(c, lib().bsg_rms_norm(
+        x.data_ptr(), ldx, _address(residual), ldr, weight.data_ptr(), eps, T, d, code,
+        _address(h), ldh, y.data_ptr(), ldy, ycode, _address(y_scale), _address(rstd), stream))
 
 
 def rms_norm_backward_workspace_bytes(T: int, d: int) -> int:
@@ -412,37 +432,46 @@ def rms_norm_backward(dy, h, weight, rstd, dx, dweight, workspace, dh=None):
     """dx (of x and of the residual alike) and dweight (fp32) from dy and,
     when given, the gradient dh that reaches h along the residual stream."""
     c = "rms_norm_backward"
-    _on_device(c, dy, h, weight, rstd, dx, dweight, workspace, dh)
-    _need(dy.dim() == 2, c, "dy must be a [T, d] tensor")
-    T, d = dy.shape
-    lds = [_rows(c, n, t, T, d, dy.dtype) if t is not None else 0
-           for n, t in (("dy", dy), ("dh", dh), ("h", h), ("dx", dx))]
-    _vector(c, "weight", weight, d, dy.dtype)
+    stream = _current(c, (dy, h, weight, rstd, dx, dweight, workspace, dh))
+    shape, dt = dy.shape, dy.dtype
+    if len(shape) != 2:
+        _fail(c, "dy must be a [T, d] tensor")
+    T, d = shape
+    lddy = _rows(c, "dy", dy, shape, dt)
+    ldh = _rows(c, "h", h, shape, dt)
+    lddx = _rows(c, "dx", dx, shape, dt)
+    lddh = _rows(c, "dh", dh, shape, dt) if dh is not None else 0
+    _vector(c, "weight", weight, d, dt)
     _vector(c, "rstd", rstd, T, torch.float32)
     _vector(c, "dweight", dweight, d, torch.float32)
-    _check(c, lib().bsg_rms_norm_backward(_ptr(dy), lds[0], _ptr(dh), lds[1], _ptr(h), lds[2],
-                                          _ptr(weight), _ptr(rstd), T, d, dtype_code(dy),
-                                          _ptr(dx), lds[3], _ptr(dweight), _ptr(workspace),
-                                          _nbytes(workspace), _stream()))
+    _check(c, lib().bsg_rms_norm_backward(
+        dy.data_ptr(), lddy, _address(dh), lddh, h.data_ptr(), ldh, weight.data_ptr(),
+        rstd.data_ptr(), T, d, dtype_code(dy), dx.data_ptr(), lddx, dweight.data_ptr(),
+        workspace.data_ptr(), _nbytes(c, workspace), stream))
 
 
 def _operand_code(t):
-    return E4M3 if t.dtype == torch.float8_e4m3fn else dtype_code(t)
+    return E4M3 if t.dtype == _F8 else dtype_code(t)
 
 
 def _matrices(call, name, t, shape, dtype):
     """(ld, stride) of one matrix an expert, [E, rows, cols] with contiguous rows."""
-    _need(t.dim() == 3 and tuple(t.shape) == tuple(shape) and t.dtype == dtype, call,
-          f"{name} must be a {list(shape)} tensor of {dtype}")
-    _need(t.stride(2) == 1 or shape[2] == 1, call, f"{name} must have contiguous rows")
-    return max(t.stride(1), shape[2]) if shape[1] == 1 else t.stride(1), t.stride(0)
+    if t.shape != shape or t.dtype != dtype:
+        _fail(call, f"{name} must be a {list(shape)} tensor of {dtype}")
+    stride, ld, one = t.stride()
+    if one != 1 and shape[2] > 1:
+        _fail(call, f"{name} must have contiguous rows")
+    return ld if shape[1] > 1 or ld > shape[2] else shape[2], stride
+
+
+def _code_of(epilogue):
+    return EPILOGUES[epilogue] if isinstance(epilogue, str) else int(epilogue)
 
 
 def grouped_gemm_workspace_bytes(M: int, K: int, N: int, E: int, epilogue="none") -> int:
     """Bytes of a workspace that lets grouped_gemm split few-row products (0:
     it never splits this one)."""
-    epi = EPILOGUES[epilogue] if isinstance(epilogue, str) else int(epilogue)
-    return int(lib().bsg_grouped_gemm_workspace_bytes(M, K, N, E, epi))
+    return int(lib().bsg_grouped_gemm_workspace_bytes(M, K, N, E, _code_of(epilogue)))
 
 
 def grouped_gemm(a, row_offsets, b, c, epilogue="none", trans_b=False, a2=None, b2=None,
@@ -454,36 +483,35 @@ def grouped_gemm(a, row_offsets, b, c, epilogue="none", trans_b=False, a2=None, 
     [M], b_scale [E, N], or [2, E, N] with b2).  c is [M, N]; two-plane
     arrays (silu_mul's aux_out, silu_mul_bwd's aux_in and c) [2, M, N]."""
     call = "grouped_gemm"
-    _on_device(call, a, row_offsets, b, c, a2, b2, a_scale, b_scale, aux_in, aux_out, workspace)
-    epi = EPILOGUES[epilogue] if isinstance(epilogue, str) else int(epilogue)
-    _need(a.dim() == 2 and b.dim() == 3 and c.dim() in (2, 3), call,
-          "a is [M, K], b one matrix an expert, c [M, N]")
+    stream = _current(call, (a, row_offsets, b, c, a2, b2, a_scale, b_scale, aux_in, aux_out,
+                             workspace))
+    epi = _code_of(epilogue)
+    if a.dim() != 2 or b.dim() != 3:
+        _fail(call, "a is [M, K], b one matrix an expert")
     M, K = a.shape
     E, N = b.shape[0], b.shape[1 if trans_b else 2]
-    lda = _rows(call, "a", a, M, K, a.dtype)
+    lda = _rows(call, "a", a, a.shape, a.dtype)
     ldb, stride = _matrices(call, "b", b, (E, N, K) if trans_b else (E, K, N), a.dtype)
     _vector(call, "row_offsets", row_offsets, E + 1, torch.int32)
-    if a2 is not None:
-        _need(_rows(call, "a2", a2, M, K, a.dtype) == lda, call, "a2 must be laid out as a")
-    if b2 is not None:
-        _need(_matrices(call, "b2", b2, b.shape, a.dtype) == (ldb, stride), call,
-              "b2 must be laid out as b")
+    if a2 is not None and _rows(call, "a2", a2, a.shape, a.dtype) != lda:
+        _fail(call, "a2 must be laid out as a")
+    if b2 is not None and _matrices(call, "b2", b2, b.shape, a.dtype) != (ldb, stride):
+        _fail(call, "b2 must be laid out as b")
     if a_scale is not None:
         _vector(call, "a_scale", a_scale, M, torch.float32)
     if b_scale is not None:
         n = (2 if b2 is not None else 1) * E * N
-        _need(b_scale.numel() == n and b_scale.dtype == torch.float32 and b_scale.is_contiguous(),
-              call, f"b_scale must be {n} contiguous fp32 values")
+        if b_scale.numel() != n or b_scale.dtype != torch.float32 or not b_scale.is_contiguous():
+            _fail(call, f"b_scale must be {n} contiguous fp32 values")
 
     def planes(name, t, two, ld=None):
-        one = t
-        if two:
-            _need(t.dim() == 3 and t.shape[0] == 2, call, f"{name} must be [2, {M}, {N}]")
-            one = t[0]
-        got = _rows(call, name, one, M, N, c.dtype)
-        _need(ld is None or got == ld, call, f"{name} must be laid out as c")
-        _need(not two or M == 0 or t.stride(0) == M * (got if ld is None else ld), call,
-              f"the second plane of {name} must follow the first")
+        if t.dim() != (3 if two else 2) or (two and t.shape[0] != 2):
+            _fail(call, f"{name} must be a [{'2, ' if two else ''}{M}, {N}] tensor")
+        got = _rows(call, name, t[0] if two else t, (M, N), c.dtype)
+        if ld is not None and got != ld:
+            _fail(call, f"{name} must be laid out as c")
+        if two and M and t.stride(0) != M * got:
+            _fail(call, f"the second plane of {name} must follow the first")
         return got
 
     ldc = planes("c", c, epi == EPI_SILU_MUL_BWD)
@@ -492,37 +520,45 @@ def grouped_gemm(a, row_offsets, b, c, epilogue="none", trans_b=False, a2=None, 
     if aux_out is not None:
         planes("aux_out", aux_out, epi == EPI_SILU_MUL, ldc)
     _check(call, lib().bsg_grouped_gemm(
-        _ptr(a), _ptr(a2), lda, _ptr(a_scale), _ptr(b), _ptr(b2), ldb, stride, _ptr(b_scale),
-        int(bool(trans_b)), _ptr(row_offsets), E, M, K, N, epi, _ptr(aux_in), _ptr(c), ldc,
-        dtype_code(c), _ptr(aux_out), _operand_code(a), _ptr(workspace), _nbytes(workspace),
-        _stream()))
+        a.data_ptr(), _address(a2), lda, _address(a_scale), b.data_ptr(), _address(b2), ldb,
+        stride, _address(b_scale), int(bool(trans_b)), row_offsets.data_ptr(), E, M, K, N, epi,
+        _address(aux_in), c.data_ptr(), ldc, dtype_code(c), _address(aux_out), _operand_code(a),
+        _address(workspace), _nbytes(call, workspace), stream))
 
 
 def grouped_wgrad(a, dmat, row_offsets, c):
     """c[e] = a[rows of e]^T @ dmat[rows of e]: c is an [E, K, N] view with
     contiguous rows, of a's type or fp32."""
     call = "grouped_wgrad"
-    _on_device(call, a, dmat, row_offsets, c)
-    _need(a.dim() == 2 and dmat.dim() == 2 and c.dim() == 3, call,
-          "a is [M, K], dmat [M, N], c one matrix an expert")
+    stream = _current(call, (a, dmat, row_offsets, c))
+    if a.dim() != 2 or dmat.dim() != 2 or c.dim() != 3:
+        _fail(call, "a is [M, K], dmat [M, N], c one matrix an expert")
     M, K = a.shape
     N, E = dmat.shape[1], c.shape[0]
-    lda = _rows(call, "a", a, M, K, a.dtype)
-    ldd = _rows(call, "dmat", dmat, M, N, a.dtype)
+    lda = _rows(call, "a", a, a.shape, a.dtype)
+    ldd = _rows(call, "dmat", dmat, (M, N), a.dtype)
     ldc, stride = _matrices(call, "c", c, (E, K, N), c.dtype)
     _vector(call, "row_offsets", row_offsets, E + 1, torch.int32)
-    _check(call, lib().bsg_grouped_wgrad(_ptr(a), lda, _ptr(dmat), ldd, _ptr(row_offsets), E, M,
-                                         K, N, _ptr(c), ldc, max(stride, 1), dtype_code(c),
-                                         dtype_code(a), _stream()))
+    _check(call, lib().bsg_grouped_wgrad(
+        a.data_ptr(), lda, dmat.data_ptr(), ldd, row_offsets.data_ptr(), E, M, K, N, c.data_ptr(),
+        ldc, stride, dtype_code(c), dtype_code(a), stream))
 
 
 def _tensor_list(call, name, tensors):
-    for t in tensors:
-        _need(t.is_contiguous(), call, f"{name} must be contiguous")
-    n = len(tensors)
-    return ((C.c_void_p * n)(*[t.data_ptr() for t in tensors]),
-            (C.c_int64 * n)(*[t.numel() for t in tensors]),
-            (C.c_int * n)(*[dtype_code(t) for t in tensors]))
+    """Addresses, sizes and type codes of a list of gradients, as C arrays."""
+    T = torch.Tensor
+    if not all(map(T.is_contiguous, tensors)):
+        _fail(call, f"{name} must be contiguous")
+    try:
+        codes = [_CODES[t.dtype] for t in tensors]
+    except KeyError as e:
+        raise TypeError(f"{call}: unsupported dtype {e}") from None
+    return (array.array("Q", map(T.data_ptr, tensors)), array.array("q", map(T.numel, tensors)),
+            array.array("i", codes))
+
+
+def _start(a):
+    return a.buffer_info()[0] if a else None
 
 
 def grad_norm_workspace_bytes() -> int:
@@ -532,26 +568,29 @@ def grad_norm_workspace_bytes() -> int:
 def grad_norm(grads, norm, workspace):
     """norm (one fp32) = the 2-norm over all values of the tensors in grads."""
     c = "grad_norm"
-    _on_device(c, norm, workspace, *grads)
-    _need(norm.numel() == 1 and norm.dtype == torch.float32, c, "norm must be one fp32 value")
+    stream = _current(c, (norm, workspace, *grads))
+    if norm.numel() != 1 or norm.dtype != torch.float32:
+        _fail(c, "norm must be one fp32 value")
     ptrs, counts, dtypes = _tensor_list(c, "grads", grads)
-    _check(c, lib().bsg_grad_norm(ptrs, counts, dtypes, len(grads), _ptr(norm), _ptr(workspace),
-                                  _nbytes(workspace), _stream()))
+    _check(c, lib().bsg_grad_norm(_start(ptrs), _start(counts), _start(dtypes), len(grads),
+                                  norm.data_ptr(), workspace.data_ptr(), _nbytes(c, workspace),
+                                  stream))
 
 
 def grad_clip(grads, norm, max_norm, out=None):
     """Scale grads by min(1, max_norm / norm), in place or into out."""
     c = "grad_clip"
-    _on_device(c, norm, *grads, *(out or ()))
-    _need(norm.numel() == 1 and norm.dtype == torch.float32, c, "norm must be one fp32 value")
+    stream = _current(c, (norm, *grads, *(out or ())))
+    if norm.numel() != 1 or norm.dtype != torch.float32:
+        _fail(c, "norm must be one fp32 value")
     ptrs, counts, dtypes = _tensor_list(c, "grads", grads)
     to = None
     if out is not None:
-        _need([(t.numel(), t.dtype) for t in out] == [(t.numel(), t.dtype) for t in grads], c,
-              "out must have the sizes and types of grads")
-        to = _tensor_list(c, "out", out)[0]
-    _check(c, lib().bsg_grad_clip(ptrs, to, counts, dtypes, len(grads), _ptr(norm), max_norm,
-                                  _stream()))
+        to, out_counts, out_dtypes = _tensor_list(c, "out", out)
+        if out_counts != counts or out_dtypes != dtypes:
+            _fail(c, "out must have the sizes and types of grads")
+    _check(c, lib().bsg_grad_clip(_start(ptrs), _start(to) if to else None, _start(counts),
+                                  _start(dtypes), len(grads), norm.data_ptr(), max_norm, stream))
 
 
 def stream_copy(src, dst, nbytes=None):

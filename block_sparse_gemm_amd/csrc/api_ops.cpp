@@ -145,11 +145,20 @@ static bool grouped_ld_fits(int64_t ld, int es, bool k_contiguous) {
 
 static int grouped_elt_bytes(int dtype) { return dtype == BSG_E4M3 ? 1 : elt_bytes(dtype); }
 
+// Compute units that the split along K is planned for (an MI355X's: the size
+// query has no stream to ask).
+constexpr int kSegmentCus = 256;
+
 size_t bsg_grouped_gemm_workspace_bytes(int64_t M, int K, int N, int E, int epilogue) {
     if (M < 0 || M > INT32_MAX || K < 1 || K > kMaxWidth || N < 1 || N > kMaxWidth || E < 1 ||
         E > BSG_MAX_EXPERTS || epilogue < BSG_EPI_NONE || epilogue > BSG_EPI_SILU_MUL_BWD)
         return 0;
-    return 0;
+    if (M == 0) return 0;
+    // the most segments that any type has on a device of this many compute units
+    int n = 1;
+    for (const int dtype : {BSG_F32, BSG_BF16, BSG_E4M3})
+        n = std::max(n, bsg::grouped_segments(M, K, N, E, epilogue, dtype, kSegmentCus));
+    return n == 1 ? 0 : (size_t)n * M * N * (epilogue == BSG_EPI_SILU_MUL ? 2 : 1) * sizeof(float);
 }
 
 bsg_status bsg_grouped_gemm(const void* a, const void* a2, int64_t lda, const float* a_scale,
@@ -219,9 +228,9 @@ bsg_status bsg_grouped_gemm(const void* a, const void* a2, int64_t lda, const fl
     if (M == 0) return ok();
     REQUIRE_VEC_PTR(a);
     REQUIRE_VEC_PTR(c);
-    // (tiles of the narrowest kind: 16 rows x 32 columns)
+    // tiles of the smaller kind (128 x 128), in most segments
     const int64_t ne = std::min<int64_t>(E, M);
-    if (((M + 15 * ne) / 16) * ((N + 31) / 32) > INT32_MAX)
+    if (((M + 127 * ne) / 128) * ((N + 127) / 128) * bsg::kMaxSegments > INT32_MAX)
         return fail(BSG_EUNSUPPORTED, "too many tiles");
     bsg::GroupedParams p{};
     p.a = a;
@@ -234,8 +243,15 @@ bsg_status bsg_grouped_gemm(const void* a, const void* a2, int64_t lda, const fl
     p.row_offsets = row_offsets;
     p.c = c;
     p.aux_out = aux_out;
+    // segments as many as planned, or as the workspace holds
+    const int64_t share = M * N * (epilogue == BSG_EPI_SILU_MUL ? 2 : 1) * (int64_t)sizeof(float);
+    p.nseg = 1;
+    if (workspace && (int64_t)(workspace_bytes / 2) >= share)
+        p.nseg = (int)std::min<int64_t>(
+            bsg::grouped_segments(M, K, N, E, epilogue, dtype, kSegmentCus),
+            (int64_t)workspace_bytes / share);
     p.ws = (float*)workspace;
-    p.ws_floats = workspace ? (int64_t)(workspace_bytes / sizeof(float)) : 0;
+    p.tile_rows = bsg::grouped_tile_rows(M, E, K, N, epilogue, dtype, kSegmentCus);
     p.lda = lda;
     p.ldb = ldb;
     p.ldc = ldc;
@@ -244,8 +260,6 @@ bsg_status bsg_grouped_gemm(const void* a, const void* a2, int64_t lda, const fl
     p.K = K;
     p.N = N;
     p.E = E;
-    const hipError_t e = bsg::device_cus((hipStream_t)stream, &p.ncu);
-    if (e != hipSuccess) return hip_status(e, "grouped_gemm");
     return hip_status(bsg::launch_grouped_gemm(p, trans_b, epilogue, c_dtype, dtype,
                                                (hipStream_t)stream),
                       "grouped_gemm");

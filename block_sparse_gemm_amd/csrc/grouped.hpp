@@ -171,6 +171,14 @@ __device__ __forceinline__ void dma16_range(uint32_t lds_addr, u32x4 desc, uint3
                  : "memory", "scc");
 }
 
+// Wait until at most N of this wave's loads are in flight (they retire in
+// issue order).
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+    static_assert(N >= 0 && N < 64, "the counter's range");
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 
 // Both 16-byte K pieces of a stage row at once: lane half h holds pieces h
@@ -207,6 +215,40 @@ __device__ __forceinline__ void unroll(F&& f) {
 
 // --------------------------------------------------------------- the tile
 
+// Four values of the epilogue: v (and u, the second product) become the
+// output, x and y what goes beside it (saved factors; SILU_MUL_BWD: the
+// second plane); d and q are the saved factors read.
+template <int EPI>
+__device__ __forceinline__ void epilogue4(float* v, const float* u, float* x, float* y, const float* d,
+                                          const float* q) {
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+        if constexpr (EPI == kEpiGelu) {
+            v[s] = gelu_f(v[s]);
+        } else if constexpr (EPI == kEpiGeluSave) {
+            gelu_and_grad(v[s], v[s], x[s]);
+        } else if constexpr (EPI == kEpiSiluMul) {
+            v[s] = silu_f(v[s]) * u[s];
+        } else if constexpr (EPI == kEpiSiluMulSave) {
+            float sp;
+            silu_and_grad(v[s], x[s], sp);
+            y[s] = u[s] * sp;
+            v[s] = x[s] * u[s];
+        } else if constexpr (EPI == kEpiGeluBwd) {
+            v[s] *= d[s];
+        } else if constexpr (EPI == kEpiSiluMulBwd) {
+            x[s] = v[s] * d[s];
+            v[s] *= q[s];
+        }
+    }
+}
+
+// Whether the epilogue has a second and a third output.
+template <int EPI>
+constexpr bool kHasX = EPI == kEpiGeluSave || EPI == kEpiSiluMulSave || EPI == kEpiSiluMulBwd;
+template <int EPI>
+constexpr bool kHasY = EPI == kEpiSiluMulSave;
+
 // What a tile stores: rows [0, mr) x columns [n0, min(N, n0 + width)) of an
 // output whose row 0 is the tile's first row.
 struct TileOut {
@@ -219,6 +261,8 @@ struct TileOut {
     const float* a_scale;  // of tile row 0, or NULL
     const float* b_scale;  // of column 0 of the group's weights
     const float* b2_scale;
+    float* part;   // SPLIT: a K segment's sums (row 0, column 0; leading dimension N)
+    float* part2;  // and, DUAL, those of b2
     int64_t ldc;
     int mr, n0, N;
 };
@@ -227,13 +271,17 @@ struct TileOut {
 // by 64 and the second A panel is not loaded).  K of one set; sets 2: a second
 // pair of operands into the same accumulators.  op: A, B (DUAL: its second
 // panel's B) of the first set, then of the second.
-template <int DT, bool AK, bool BK, int EPI, int OUT, bool HALF>
+// STAGES K-tiles in the ring, of 32 KB each (HALF: 24 KB).
+// SPLIT: the sums of a K segment go to o.part instead of the epilogue.
+template <int DT, bool AK, bool BK, int EPI, int OUT, bool HALF, int STAGES, bool SPLIT>
 __device__ __forceinline__ void ragged_tile(char* smem, const Operand (*op)[3], int64_t lda_b,
                                              int64_t ldb_b, int64_t K, int sets, const TileOut& o) {
     constexpr int ES = GElt<DT>::kBytes, KT = GElt<DT>::kKt;
     constexpr bool DUAL = EPI == kEpiSiluMul || EPI == kEpiSiluMulSave;
     constexpr int LPT = HALF ? kLoadsPerTile - 2 : kLoadsPerTile;
-    constexpr int NH = HALF ? 1 : 2, NMI = HALF ? 2 : 4, NI = DUAL ? 2 : 4;
+    constexpr int NMI = HALF ? 2 : 4, NI = DUAL ? 2 : 4;
+    constexpr int PA = HALF ? 1 : 2;  // A panels; B's two follow them in a stage
+    constexpr int STAGE_BYTES = (PA + 2) * kPanelBytes;
     static_assert(DT != kE4m3 || (AK && BK), "e4m3 operands are K-contiguous");
     lds_t* lds = (lds_t*)smem;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -286,14 +334,15 @@ __device__ __forceinline__ void ragged_tile(char* smem, const Operand (*op)[3], 
         constexpr bool KC = i == 0 ? AK : BK;
         if constexpr (HALF && pnl == 1) return;
         else
-            dma16_range<pnl * kPanelBytes + sg * 1024>(
+            dma16_range<(pnl < 2 ? pnl : PA + pnl - 2) * kPanelBytes + sg * 1024>(
                 lds_lt, desc[i], KC ? off[pnl][sg] | tail : off[pnl][sg], KC ? soff : 0u);
     };
     // Selects, not branches: behind a branch the compiler gathers the MFMAs
     // that should run among the loads.
     auto next = [&]() {
         ++lt;
-        lds_lt = lds0 + (lt % kStages) * kStageBytes;
+        lds_lt += STAGE_BYTES;
+        if (lds_lt == lds0 + STAGES * STAGE_BYTES) lds_lt = lds0;
         const bool over = lt >= nk, swap = TWO && lt == nk1;
         soff = over || swap ? 0u : soff + kRowBytes;
         tail = lt == nk1 - 1 || lt == nk - 1 ? behind : 0u;
@@ -323,38 +372,40 @@ __device__ __forceinline__ void ragged_tile(char* smem, const Operand (*op)[3], 
 #pragma unroll
             for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
 
-    // fragment f (0..NMI-1: A, then four of B), K piece c of K-tile t
-    auto read1 = [&](int t, int c, int f, u32x4 (*af)[2], u32x4 (*bf)[2]) {
-        const lds_t* st = lds + (t % kStages) * kStageBytes;
+    // fragment f (0..NMI-1: A, then four of B), K piece c of the K-tile in stage st
+    auto read1 = [&](const lds_t* st, int c, int f, u32x4 (*af)[2], u32x4 (*bf)[2]) {
         if (f < NMI) {
             af[f][c] = HALF ? frag<LT, AK>(st, 64 * wm + 32 * f, c)
                             : frag<LT, AK>(st + wm * kPanelBytes, 32 * f, c);
         } else {
             const int ni = f - NMI;
-            const int pnl = DUAL ? 2 + (ni >> 1) : 2 + wn;
+            const int pnl = PA + (DUAL ? ni >> 1 : wn);
             const int row = DUAL ? wn * 64 + 32 * (ni & 1) : 32 * ni;
             bf[ni][c] = frag<LT, BK>(st + pnl * kPanelBytes, row, c);
         }
     };
     u32x4 af[2][NMI][2], bf[2][4][2];
+    int rd = 0;  // byte of the stage that the next step reads
     // One K-tile: its MFMAs, and among them the fragment reads of the next
-    // one (published by the barrier before) and the loads kStages ahead into
+    // one (published by the barrier before) and the loads STAGES ahead into
     // the stage that this K-tile's fragments have left.  Behind the last
     // K-tile the loads are out of range and bring zeros, so every step is the
     // same: no branch around the accumulators, one wait count throughout, and
     // an odd number of K-tiles ends with one of zeros.
-    auto step = [&](int t, auto cur) {
+    auto step = [&](auto cur) {
         constexpr int c0 = decltype(cur)::value, c1 = 1 - c0;
         // fragment reads, MFMA groups, and the groups the reads are spread over:
         // the last ones have no reads, so the next barrier finds them returned
         constexpr int NR = 2 * (NMI + 4), GROUPS = NMI * 4, READ = GROUPS * 3 / 4;
-        wait_tiles<LPT>(kStages - 2);
+        wait_loads<(STAGES - 2) * LPT>();
         __syncthreads();
+        rd += STAGE_BYTES;
+        if (rd == STAGES * STAGE_BYTES) rd = 0;
         unroll<GROUPS>([&](auto gc) {
             constexpr int g = decltype(gc)::value;
 #pragma unroll
             for (int r = g * NR / READ; r < (g + 1) * NR / READ && r < NR; ++r)
-                read1(t + 1, r & 1, r >> 1, af[c1], bf[c1]);
+                read1(lds + rd, r & 1, r >> 1, af[c1], bf[c1]);
             if constexpr (HALF) dma(gc);
             else if constexpr (g % 2 == 0) dma(std::integral_constant<int, g / 2>{});
             if constexpr (g == GROUPS - 1) next();
@@ -363,61 +414,83 @@ __device__ __forceinline__ void ragged_tile(char* smem, const Operand (*op)[3], 
         });
     };
     if (nk > 0) {
-        for (int t = 0; t < kStages; ++t) {
+        for (int t = 0; t < STAGES; ++t) {
             unroll<kLoadsPerTile>(dma);
             next();
         }
-        wait_tiles<LPT>(kStages - 1);
+        wait_loads<(STAGES - 1) * LPT>();
         __syncthreads();
 #pragma unroll
         for (int f = 0; f < NMI + 4; ++f) {
-            read1(0, 0, f, af[0], bf[0]);
-            read1(0, 1, f, af[0], bf[0]);
+            read1(lds, 0, f, af[0], bf[0]);
+            read1(lds, 1, f, af[0], bf[0]);
         }
         for (int kt = 0; kt < nk; kt += 2) {
-            step(kt, std::integral_constant<int, 0>{});
-            step(kt + 1, std::integral_constant<int, 1>{});
+            step(std::integral_constant<int, 0>{});
+            step(std::integral_constant<int, 1>{});
         }
-        wait_tiles<LPT>(0);  // the last (empty) loads still write their stages
+        wait_loads<0>();  // the last (empty) loads still write their stages
     }
 
-    // ---- epilogue: bf16 results go through LDS, 64 rows at a time and
-    // staged as gemm_tile stages them, so that stores write whole rows of 256
-    // (DUAL: 128) bytes; fp32 results are stored from the accumulators
+    const int wcol = o.n0 + wn * (DUAL ? 64 : 128);  // the wave's first column
+
+    // ---- a K segment: fp32 sums as they are, for the launch that adds them
+    if constexpr (SPLIT) {
+#pragma unroll
+        for (int mi = 0; mi < NMI; ++mi) {
+            const int row = (HALF ? 64 : 128) * wm + 32 * mi + l32;
+#pragma unroll
+            for (int ni = 0; ni < 4; ++ni)
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    const int col = wcol + 32 * (DUAL ? ni & 1 : ni) + 8 * g + 4 * lh;
+                    float* to = DUAL && ni >= 2 ? o.part2 : o.part;
+                    if (row < o.mr && col < o.N)
+                        *(f32x4*)(to + (int64_t)row * o.N + col) =
+                            f32x4{acc[mi][ni][4 * g], acc[mi][ni][4 * g + 1], acc[mi][ni][4 * g + 2],
+                                  acc[mi][ni][4 * g + 3]};
+                }
+        }
+        return;
+    }
+
+    // ---- epilogue: bf16 results go through LDS, 32 rows at a time, so that
+    // stores write whole rows of 256 (DUAL: 128) bytes; fp32 results are
+    // stored from the accumulators.  Chunk c of staged row r lies at slot
+    // c ^ (r & MASK), which spreads both the writes and the reads over all
+    // banks.
     constexpr bool STAGE = OUT == kBf16;
     constexpr int OES = OUT == kBf16 ? 2 : 4;
     constexpr int ROWB = DUAL ? 128 : 256;  // bytes of a staged row
     constexpr int MASK = ROWB / 16 - 1;
     if constexpr (STAGE) __syncthreads();  // the operand ring is free
-    lds_t* region = lds + wave * (kLdsBytes / 4);
-    const int wcol = o.n0 + wn * (DUAL ? 64 : 128);  // the wave's first column
+    static_assert(4 * (DUAL ? 3 : 2) * 32 * ROWB <= STAGES * STAGE_BYTES, "staging fits the ring");
+    lds_t* region = lds + wave * ((DUAL ? 3 : 2) * 32 * ROWB);
     if (wcol >= o.N) return;
-    auto put = [&](int sub, int row, int chunk, const float* v) {
-        *(__attribute__((address_space(3))) u32x2*)(region + sub * 64 * ROWB + row * ROWB +
-                                                      ((chunk ^ (row & MASK)) << 4) + lh * 8) =
+    auto put = [&](int sub, int chunk, const float* v) {  // row l32
+        *(__attribute__((address_space(3))) u32x2*)(region + sub * 32 * ROWB + l32 * ROWB +
+                                                      ((chunk ^ (l32 & MASK)) << 4) + lh * 8) =
             u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
     };
     auto flush = [&](int sub, char* base, int trow) {
         constexpr int CH = ROWB / 16, RPI = kWave / CH;  // rows an instruction
         const int chunk = lane % CH;
         const int col = wcol + chunk * 8;
-#pragma unroll 4
-        for (int rr = 0; rr < 64 / RPI; ++rr) {
+#pragma unroll
+        for (int rr = 0; rr < 32 / RPI; ++rr) {
             const int row = RPI * rr + lane / CH;
             const u32x4 u = *(const __attribute__((address_space(3))) u32x4*)(
-                region + sub * 64 * ROWB + row * ROWB + ((chunk ^ (row & MASK)) << 4));
+                region + sub * 32 * ROWB + row * ROWB + ((chunk ^ (row & MASK)) << 4));
             if (trow + row < o.mr && col < o.N)
                 __builtin_nontemporal_store(u, (u32x4*)(base + ((int64_t)(trow + row) * o.ldc + col) * 2));
         }
     };
 #pragma unroll
-    for (int h = 0; h < NH; ++h) {
-        const int trow = HALF ? 64 * wm : 128 * wm + 64 * h;
+    for (int mi = 0; mi < NMI; ++mi) {
+        const int trow = (HALF ? 64 : 128) * wm + 32 * mi;  // the slab's first row in the tile
         if (trow >= o.mr) break;
-#pragma unroll
-        for (int a = 0; a < 2; ++a) {
-            const int mi = 2 * h + a;
-            const int row = trow + 32 * a + l32;
+        {
+            const int row = trow + l32;
             const bool rin = row < o.mr;
             float sa = 1.0f;
             if constexpr (DT == kE4m3) sa = rin ? o.a_scale[row] : 0.0f;
@@ -445,46 +518,19 @@ __device__ __forceinline__ void ragged_tile(char* smem, const Operand (*op)[3], 
                             for (int s = 0; s < 4; ++s) u[s] *= sa * s2[s];
                         }
                     }
-                    float x[4], y[4];  // further outputs
-                    if constexpr (EPI == kEpiGelu) {
-#pragma unroll
-                        for (int s = 0; s < 4; ++s) v[s] = gelu_f(v[s]);
-                    } else if constexpr (EPI == kEpiGeluSave) {
-#pragma unroll
-                        for (int s = 0; s < 4; ++s) gelu_and_grad(v[s], v[s], x[s]);
-                    } else if constexpr (EPI == kEpiSiluMul) {
-#pragma unroll
-                        for (int s = 0; s < 4; ++s) v[s] = silu_f(v[s]) * u[s];
-                    } else if constexpr (EPI == kEpiSiluMulSave) {
-#pragma unroll
-                        for (int s = 0; s < 4; ++s) {
-                            float sp;
-                            silu_and_grad(v[s], x[s], sp);
-                            y[s] = u[s] * sp;
-                            v[s] = x[s] * u[s];
-                        }
-                    } else if constexpr (EPI == kEpiGeluBwd) {
-                        float d[4] = {0, 0, 0, 0};
+                    float x[4], y[4], d[4] = {0, 0, 0, 0}, q[4] = {0, 0, 0, 0};
+                    if constexpr (EPI == kEpiGeluBwd || EPI == kEpiSiluMulBwd) {
                         if (in) load4<OUT>(o.aux_in + at, d);
-#pragma unroll
-                        for (int s = 0; s < 4; ++s) v[s] *= d[s];
-                    } else if constexpr (EPI == kEpiSiluMulBwd) {
-                        float d[4] = {0, 0, 0, 0}, q[4] = {0, 0, 0, 0};
-                        if (in) load4<OUT>(o.aux_in + at, d);
-                        if (in) load4<OUT>(o.aux_in2 + at, q);
-#pragma unroll
-                        for (int s = 0; s < 4; ++s) {
-                            x[s] = v[s] * d[s];
-                            v[s] *= q[s];
-                        }
                     }
-                    constexpr bool X = EPI == kEpiGeluSave || EPI == kEpiSiluMulSave || EPI == kEpiSiluMulBwd;
-                    constexpr bool Y = EPI == kEpiSiluMulSave;
+                    if constexpr (EPI == kEpiSiluMulBwd) {
+                        if (in) load4<OUT>(o.aux_in2 + at, q);
+                    }
+                    epilogue4<EPI>(v, u, x, y, d, q);
+                    constexpr bool X = kHasX<EPI>, Y = kHasY<EPI>;
                     if constexpr (STAGE) {
-                        const int r = 32 * a + l32, chunk = 4 * ni + g;
-                        put(0, r, chunk, v);
-                        if constexpr (X) put(1, r, chunk, x);
-                        if constexpr (Y) put(2, r, chunk, y);
+                        put(0, 4 * ni + g, v);
+                        if constexpr (X) put(1, 4 * ni + g, x);
+                        if constexpr (Y) put(2, 4 * ni + g, y);
                     } else if (in) {
                         store4<OUT>(o.out + at, v);
                         if constexpr (X) store4<OUT>((EPI == kEpiSiluMulBwd ? o.out2 : o.aux_out) + at, x);
@@ -511,30 +557,51 @@ __device__ __forceinline__ void ragged_tile(char* smem, const Operand (*op)[3], 
 // both operands' panels.
 constexpr int kGroupedRows = 8;
 
-template <int DT, bool BK, int EPI, int OUT>
-__global__ __launch_bounds__(kGemmThreads, 1) void grouped_gemm_kernel(GroupedParams P) {
+// H: rows of a tile.  256: one workgroup a compute unit, a group's last rows
+// (at most 128) as a tile of half the height.  128: two workgroups a compute
+// unit, one's loads and stores beside the other's products.
+template <int H>
+struct TileShape {
+    static constexpr int kHalfStages = H == 256 ? 5 : 3;
+    static constexpr int kLds = H == 256 ? kStages * kStageBytes : 3 * 3 * kPanelBytes;
+    static constexpr int kPerCu = H == 256 ? 1 : 2;
+};
+
+template <int DT, bool BK, int EPI, int OUT, int H, bool SPLIT>
+__global__ __launch_bounds__(kGemmThreads, TileShape<H>::kPerCu) void grouped_gemm_kernel(GroupedParams P) {
     constexpr int ES = GElt<DT>::kBytes, KT = GElt<DT>::kKt;
     constexpr bool DUAL = EPI == kEpiSiluMul || EPI == kEpiSiluMulSave;
     constexpr int OES = OUT == kBf16 ? 2 : 4;
-    __shared__ __attribute__((aligned(1024))) char smem[kLdsBytes];
+    __shared__ __attribute__((aligned(1024))) char smem[TileShape<H>::kLds];
     constexpr int W = DUAL ? 128 : 256;
     const int tn = (P.N + W - 1) / W;
-    const int ntiles = row_tiles_of<256>(P.row_offsets, P.E, P.M) * tn;
-    if ((int)blockIdx.x >= ntiles) return;
-    const Group g = group_of<256>(P.row_offsets, P.E, P.M, tn, xcd_remap(blockIdx.x, ntiles));
+    const int ntiles = row_tiles_of<H>(P.row_offsets, P.E, P.M) * tn;
+    const int nseg = SPLIT ? P.nseg : 1;
+    if ((int)blockIdx.x >= ntiles * nseg) return;
+    // segment-major: what an XCD runs at once shares one K segment of its operands
+    const int v = xcd_remap(blockIdx.x, ntiles * nseg);
+    const int seg = SPLIT ? v / ntiles : 0;
+    const Group g = group_of<H>(P.row_offsets, P.E, P.M, tn, v - seg * ntiles);
     int tm, tq;
-    grouped_tile(g.local, (g.rows + 255) / 256, tn, kGroupedRows, tm, tq);
-    const int mr = min(256, g.rows - 256 * tm);
-    const int64_t row = (int64_t)g.row0 + 256 * tm;
+    grouped_tile(g.local, (g.rows + H - 1) / H, tn, kGroupedRows, tm, tq);
+    const int mr = min(H, g.rows - H * tm);
+    const int64_t row = (int64_t)g.row0 + H * tm;
     const int n0 = tq * W;
-    const int64_t lda_b = P.lda * ES, ldb_b = P.ldb * ES, K_b = (int64_t)P.K * ES;
+    int k0 = 0, K = P.K;
+    if constexpr (SPLIT) {  // the segment's K
+        const int nk = (P.K + KT - 1) / KT;
+        k0 = (int)((int64_t)nk * seg / nseg) * KT;
+        K = min(P.K, (int)((int64_t)nk * (seg + 1) / nseg) * KT) - k0;
+    }
+    const int64_t lda_b = P.lda * ES, ldb_b = P.ldb * ES, K_b = (int64_t)K * ES;
     const int64_t eb = (int64_t)g.e * P.stride_b * ES;
     auto B = [&](const void* b) {
-        if constexpr (BK) return operand_k((const char*)b + eb, n0, ldb_b, P.N - n0, K_b);
-        else return operand_n((const char*)b + eb, ldb_b, (int64_t)n0 * ES, (int64_t)P.N * ES, P.K);
+        const char* be = (const char*)b + eb + (int64_t)k0 * (BK ? ES : ldb_b);
+        if constexpr (BK) return operand_k(be, n0, ldb_b, P.N - n0, K_b);
+        else return operand_n(be, ldb_b, (int64_t)n0 * ES, (int64_t)P.N * ES, K);
     };
-    const Operand op[2][3] = {{operand_k(P.a, row, lda_b, mr, K_b), B(P.b), B(P.b2)},
-                              {operand_k(P.a2, row, lda_b, mr, K_b), B(P.b2), B(P.b2)}};
+    auto A = [&](const void* a) { return operand_k((const char*)a + (int64_t)k0 * ES, row, lda_b, mr, K_b); };
+    const Operand op[2][3] = {{A(P.a), B(P.b), B(P.b2)}, {A(P.a2), B(P.b2), B(P.b2)}};
     TileOut o{};
     o.ldc = P.ldc;
     o.mr = mr;
@@ -552,22 +619,82 @@ __global__ __launch_bounds__(kGemmThreads, 1) void grouped_gemm_kernel(GroupedPa
         o.b_scale = P.b_scale + (int64_t)g.e * P.N;
         o.b2_scale = o.b_scale + (int64_t)P.E * P.N;
     }
+    if constexpr (SPLIT) {
+        const int64_t share = P.M * P.N;
+        o.part = P.ws + (int64_t)seg * (DUAL ? 2 : 1) * share + row * P.N;
+        o.part2 = o.part + share;
+    }
     const int sets = EPI == kEpiNone && P.a2 ? 2 : 1;
-    if (mr <= 128)
-        ragged_tile<DT, true, BK, EPI, OUT, true>(smem, op, lda_b, ldb_b, P.K, sets, o);
-    else
-        ragged_tile<DT, true, BK, EPI, OUT, false>(smem, op, lda_b, ldb_b, P.K, sets, o);
+    if constexpr (H == 256) {
+        if (mr > 128) {
+            ragged_tile<DT, true, BK, EPI, OUT, false, kStages, SPLIT>(smem, op, lda_b, ldb_b, K, sets, o);
+            return;
+        }
+    }
+    ragged_tile<DT, true, BK, EPI, OUT, true, TileShape<H>::kHalfStages, SPLIT>(smem, op, lda_b, ldb_b,
+                                                                                K, sets, o);
+}
+
+// The second launch of a split product: a workgroup a row and 1024 columns,
+// the segments' sums added in order, then scales and epilogue as in the tile.
+template <int DT, int EPI, int OUT>
+__global__ __launch_bounds__(kGemmThreads) void grouped_join_kernel(GroupedParams P) {
+    constexpr bool DUAL = EPI == kEpiSiluMul || EPI == kEpiSiluMulSave;
+    constexpr int OES = OUT == kBf16 ? 2 : 4;
+    const int64_t row = blockIdx.x;
+    const int first = P.row_offsets[0], end = P.row_offsets[P.E];
+    if (row < first || row >= end) return;  // a row of no group
+    const int col = (blockIdx.y * kGemmThreads + threadIdx.x) * 4;
+    if (col >= P.N) return;
+    const int64_t share = P.M * P.N;
+    const float* part = P.ws + row * P.N + col;
+    float v[4] = {0, 0, 0, 0}, u[4] = {0, 0, 0, 0};
+#pragma unroll 4
+    for (int i = 0; i < P.nseg; ++i) {
+        const f32x4 p = *(const f32x4*)(part + (int64_t)i * (DUAL ? 2 : 1) * share);
+#pragma unroll
+        for (int s = 0; s < 4; ++s) v[s] += p[s];
+        if constexpr (DUAL) {
+            const f32x4 p2 = *(const f32x4*)(part + (int64_t)(2 * i + 1) * share);
+#pragma unroll
+            for (int s = 0; s < 4; ++s) u[s] += p2[s];
+        }
+    }
+    if constexpr (DT == kE4m3) {
+        int lo = 0, hi = P.E - 1;  // the last expert that starts at or before the row
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) / 2;
+            if (P.row_offsets[mid] <= row) lo = mid;
+            else hi = mid - 1;
+        }
+        const float sa = P.a_scale[row];
+        const float* sb = P.b_scale + (int64_t)lo * P.N + col;
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+            v[s] *= sa * sb[s];
+            if constexpr (DUAL) u[s] *= sa * sb[(int64_t)P.E * P.N + s];
+        }
+    }
+    const int64_t at = (row * P.ldc + col) * OES, plane = P.M * P.ldc * OES;
+    float x[4], y[4], d[4] = {0, 0, 0, 0}, q[4] = {0, 0, 0, 0};
+    if constexpr (EPI == kEpiGeluBwd || EPI == kEpiSiluMulBwd) load4<OUT>((const char*)P.aux_in + at, d);
+    if constexpr (EPI == kEpiSiluMulBwd) load4<OUT>((const char*)P.aux_in + plane + at, q);
+    epilogue4<EPI>(v, u, x, y, d, q);
+    store4<OUT>((char*)P.c + at, v);
+    if constexpr (EPI == kEpiSiluMulBwd) store4<OUT>((char*)P.c + plane + at, x);
+    else if constexpr (kHasX<EPI>) store4<OUT>((char*)P.aux_out + at, x);
+    if constexpr (kHasY<EPI>) store4<OUT>((char*)P.aux_out + plane + at, y);
 }
 
 // Weight gradients: C_e [K x N], the reduction along the group's rows; both
 // operands are read as they lie, row by row.  Groups in order, a group's
 // tiles four high; groups without rows store zeros.
-template <int DT, int OUT>
-__global__ __launch_bounds__(kGemmThreads, 1) void grouped_wgrad_kernel(GroupedParams P) {
+template <int DT, int OUT, int H>
+__global__ __launch_bounds__(kGemmThreads, TileShape<H>::kPerCu) void grouped_wgrad_kernel(GroupedParams P) {
     constexpr int ES = GElt<DT>::kBytes, KT = GElt<DT>::kKt;
     constexpr int OES = OUT == kBf16 ? 2 : 4;
-    __shared__ __attribute__((aligned(1024))) char smem[kLdsBytes];
-    const int tk = (P.K + 255) / 256, tn = (P.N + 255) / 256;
+    __shared__ __attribute__((aligned(1024))) char smem[TileShape<H>::kLds];
+    const int tk = (P.K + H - 1) / H, tn = (P.N + 255) / 256;
     const int per = tk * tn, ntiles = P.E * per;
     const int t = xcd_chunked(blockIdx.x, ntiles, kDstdChunk);
     const int e = t / per;
@@ -580,19 +707,24 @@ __global__ __launch_bounds__(kGemmThreads, 1) void grouped_wgrad_kernel(GroupedP
     const int64_t lda_b = P.lda * ES, ldb_b = P.ldb * ES;
     const char* A = (const char*)P.a + (int64_t)row0 * lda_b;
     const char* D = (const char*)P.b + (int64_t)row0 * ldb_b;
-    const Operand oa = operand_n(A, lda_b, (int64_t)tm * 256 * ES, (int64_t)P.K * ES, rows);
+    const Operand oa = operand_n(A, lda_b, (int64_t)tm * H * ES, (int64_t)P.K * ES, rows);
     const Operand ob = operand_n(D, ldb_b, (int64_t)tq * 256 * ES, (int64_t)P.N * ES, rows);
     const Operand op[2][3] = {{oa, ob, ob}, {oa, ob, ob}};
     TileOut o{};
     o.ldc = P.ldc;
-    o.mr = min(256, P.K - 256 * tm);
+    o.mr = min(H, P.K - H * tm);
     o.n0 = tq * 256;
     o.N = P.N;
-    o.out = (char*)P.c + ((int64_t)e * P.stride_b + (int64_t)tm * 256 * P.ldc) * OES;
-    if (o.mr <= 128)
-        ragged_tile<DT, false, false, kEpiNone, OUT, true>(smem, op, lda_b, ldb_b, rows, 1, o);
-    else
-        ragged_tile<DT, false, false, kEpiNone, OUT, false>(smem, op, lda_b, ldb_b, rows, 1, o);
+    o.out = (char*)P.c + ((int64_t)e * P.stride_b + (int64_t)tm * H * P.ldc) * OES;
+    if constexpr (H == 256) {
+        if (o.mr > 128) {
+            ragged_tile<DT, false, false, kEpiNone, OUT, false, kStages, false>(smem, op, lda_b, ldb_b, rows,
+                                                                                 1, o);
+            return;
+        }
+    }
+    ragged_tile<DT, false, false, kEpiNone, OUT, true, TileShape<H>::kHalfStages, false>(
+        smem, op, lda_b, ldb_b, rows, 1, o);
 }
 
 // Most tiles of M rows in E groups, `per` tiles a row tile of H rows: every
@@ -602,13 +734,30 @@ inline int64_t grouped_tiles_max(int64_t M, int E, int H, int64_t per) {
     return ((M + (int64_t)(H - 1) * ne) / H) * per;
 }
 
-template <int DT, bool BK, int EPI, int OUT>
-static hipError_t grouped_go(const GroupedParams& p, hipStream_t s) {
+template <int DT, bool BK, int EPI, int OUT, int H, bool SPLIT>
+static hipError_t grouped_go_h(const GroupedParams& p, hipStream_t s) {
     constexpr int W = EPI == kEpiSiluMul || EPI == kEpiSiluMulSave ? 128 : 256;
-    const int64_t grid = grouped_tiles_max(p.M, p.E, 256, (p.N + W - 1) / W);
-    hipLaunchKernelGGL((grouped_gemm_kernel<DT, BK, EPI, OUT>), dim3((unsigned)grid),
+    const int64_t grid = grouped_tiles_max(p.M, p.E, H, (p.N + W - 1) / W) * (SPLIT ? p.nseg : 1);
+    hipLaunchKernelGGL((grouped_gemm_kernel<DT, BK, EPI, OUT, H, SPLIT>), dim3((unsigned)grid),
                        dim3(kGemmThreads), 0, s, p);
     return hipGetLastError();
+}
+
+template <int DT, bool BK, int EPI, int OUT>
+static hipError_t grouped_go(const GroupedParams& p, hipStream_t s) {
+    if (p.nseg > 1) {  // few rows: the segments' kernel knows no epilogue, the join does
+        constexpr bool DUAL = EPI == kEpiSiluMul || EPI == kEpiSiluMulSave;
+        constexpr int E = DUAL ? kEpiSiluMul : kEpiNone;
+        const hipError_t e = p.tile_rows == 128 ? grouped_go_h<DT, BK, E, kF32, 128, true>(p, s)
+                                                : grouped_go_h<DT, BK, E, kF32, 256, true>(p, s);
+        if (e != hipSuccess) return e;
+        hipLaunchKernelGGL((grouped_join_kernel<DT, EPI, OUT>),
+                           dim3((unsigned)p.M, (unsigned)((p.N + 4 * kGemmThreads - 1) / (4 * kGemmThreads))),
+                           dim3(kGemmThreads), 0, s, p);
+        return hipGetLastError();
+    }
+    return p.tile_rows == 128 ? grouped_go_h<DT, BK, EPI, OUT, 128, false>(p, s)
+                              : grouped_go_h<DT, BK, EPI, OUT, 256, false>(p, s);
 }
 
 }  // namespace bsg

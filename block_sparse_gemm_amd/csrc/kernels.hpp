@@ -166,14 +166,19 @@ struct GroupedParams {
     const int32_t* row_offsets;  // [E + 1]
     void* c;               // [M, N] (SILU_MUL_BWD: two planes)  [[E] K x N]
     void* aux_out;
-    float* ws;             // partial sums of the few-row kernel, or NULL
-    int64_t ws_floats;
+    float* ws;             // sums of K segments (nseg > 1): [nseg][M][N], with b2 [nseg][2][M][N]
+    int nseg;              // K segments
+    int tile_rows;         // 128 or 256
     int64_t lda, ldb, ldc;
     int64_t stride_b;      // from an expert's matrix to the next one's  [of c]
     int64_t M;
     int K, N, E;
-    int ncu;
 };
+
+constexpr int kMaxSegments = 16;
+
+int grouped_tile_rows(int64_t M, int E, int K, int N, int epi, int dtype, int ncu);
+int grouped_segments(int64_t M, int K, int N, int E, int epi, int dtype, int ncu);
 
 hipError_t launch_grouped_gemm(const GroupedParams& p, int trans_b, int epi, int c_dtype, int dtype,
                                hipStream_t stream);
