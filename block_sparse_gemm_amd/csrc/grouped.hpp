@@ -328,21 +328,36 @@ __device__ __forceinline__ void ragged_tile(char* smem, const Operand (*op)[3], 
     uint32_t tail = nk1 == 1 ? behind : 0u;   // `behind` while K-tile lt is a set's last
     const uint32_t lds0 = lds_u32(lds) + wave * kSegsPerWave * 1024;
     uint32_t lds_lt = lds0;                   // this wave's segments in K-tile lt's stage
-    auto dma = [&](auto jc) {  // load j (0..7): panel j & 3, segment j >> 2
+    // load j (0..7): panel j & 3, segment j >> 2; FAST: not a set's last K-tile
+    auto dma = [&](auto jc, auto fast) {
         constexpr int j = decltype(jc)::value, pnl = j & 3, sg = j >> 2;
         constexpr int i = pnl < 2 ? 0 : DUAL && pnl == 3 ? 2 : 1;
-        constexpr bool KC = i == 0 ? AK : BK;
+        constexpr bool KC = i == 0 ? AK : BK, TAIL = KC && !decltype(fast)::value;
         if constexpr (HALF && pnl == 1) return;
         else
             dma16_range<(pnl < 2 ? pnl : PA + pnl - 2) * kPanelBytes + sg * 1024>(
-                lds_lt, desc[i], KC ? off[pnl][sg] | tail : off[pnl][sg], KC ? soff : 0u);
+                lds_lt, desc[i], TAIL ? off[pnl][sg] | tail : off[pnl][sg], KC ? soff : 0u);
     };
-    // Selects, not branches: behind a branch the compiler gathers the MFMAs
-    // that should run among the loads.
-    auto next = [&]() {
+    auto next_stage = [&]() {
         ++lt;
         lds_lt += STAGE_BYTES;
         if (lds_lt == lds0 + STAGES * STAGE_BYTES) lds_lt = lds0;
+    };
+    // Operands [I0, I1) that move their base: one K-tile on.
+    auto advance = [&](int i0, int i1) {
+#pragma unroll
+        for (int i = i0; i < i1; ++i) {
+            if (i == 0 ? AK : BK) continue;
+            const int64_t step = KT * (i == 0 ? lda_b : ldb_b);
+            base[i] += step;
+            left[i] -= step;
+            desc[i] = descriptor(base[i], left[i]);
+        }
+    };
+    // One K-tile on, over the end of a set too.  Selects, not branches: behind
+    // a branch the compiler gathers the MFMAs that should run among the loads.
+    auto next = [&]() {
+        next_stage();
         const bool over = lt >= nk, swap = TWO && lt == nk1;
         soff = over || swap ? 0u : soff + kRowBytes;
         tail = lt == nk1 - 1 || lt == nk - 1 ? behind : 0u;
@@ -389,11 +404,13 @@ __device__ __forceinline__ void ragged_tile(char* smem, const Operand (*op)[3], 
     // One K-tile: its MFMAs, and among them the fragment reads of the next
     // one (published by the barrier before) and the loads STAGES ahead into
     // the stage that this K-tile's fragments have left.  Behind the last
-    // K-tile the loads are out of range and bring zeros, so every step is the
-    // same: no branch around the accumulators, one wait count throughout, and
-    // an odd number of K-tiles ends with one of zeros.
-    auto step = [&](auto cur) {
+    // K-tile the loads are out of range and bring zeros: one wait count
+    // throughout, and an odd number of K-tiles ends with one of zeros.  FAST
+    // steps, nearly all, stay inside a set and spend few scalar instructions,
+    // which would otherwise hold up the next MFMA.
+    auto step = [&](auto cur, auto fast) {
         constexpr int c0 = decltype(cur)::value, c1 = 1 - c0;
+        constexpr bool FAST = decltype(fast)::value;
         // fragment reads, MFMA groups, and the groups the reads are spread over:
         // the last ones have no reads, so the next barrier finds them returned
         constexpr int NR = 2 * (NMI + 4), GROUPS = NMI * 4, READ = GROUPS * 3 / 4;
@@ -406,16 +423,28 @@ __device__ __forceinline__ void ragged_tile(char* smem, const Operand (*op)[3], 
 #pragma unroll
             for (int r = g * NR / READ; r < (g + 1) * NR / READ && r < NR; ++r)
                 read1(lds + rd, r & 1, r >> 1, af[c1], bf[c1]);
-            if constexpr (HALF) dma(gc);
-            else if constexpr (g % 2 == 0) dma(std::integral_constant<int, g / 2>{});
-            if constexpr (g == GROUPS - 1) next();
+            if constexpr (HALF) dma(gc, fast);
+            else if constexpr (g % 2 == 0) dma(std::integral_constant<int, g / 2>{}, fast);
+            if constexpr (FAST) {
+                // behind the last load of A, and of B
+                if constexpr (g == (HALF ? 5 : 11)) advance(0, 1);
+                if constexpr (g == GROUPS - 1) {
+                    advance(1, NOP);
+                    soff += kRowBytes;
+                    next_stage();
+                }
+            } else {
+                if constexpr (g == GROUPS - 1) next();
+            }
             mma_stage<DT>(acc[g >> 2][g & 3], bf[c0][g & 3], af[c0][g >> 2]);
             __builtin_amdgcn_sched_barrier(0);
         });
     };
     if (nk > 0) {
+        using No = std::false_type;
+        using Yes = std::true_type;
         for (int t = 0; t < STAGES; ++t) {
-            unroll<kLoadsPerTile>(dma);
+            unroll<kLoadsPerTile>([&](auto jc) { dma(jc, No{}); });
             next();
         }
         wait_loads<(STAGES - 1) * LPT>();
@@ -426,8 +455,14 @@ __device__ __forceinline__ void ragged_tile(char* smem, const Operand (*op)[3], 
             read1(lds, 1, f, af[0], bf[0]);
         }
         for (int kt = 0; kt < nk; kt += 2) {
-            step(std::integral_constant<int, 0>{});
-            step(std::integral_constant<int, 1>{});
+            // steps whose load and the one after it are not the end of a set
+            const int fast = (lt < nk1 ? nk1 : nk) - 2 - lt;
+            for (int i = fast; i > 1; i -= 2, kt += 2) {
+                step(std::integral_constant<int, 0>{}, Yes{});
+                step(std::integral_constant<int, 1>{}, Yes{});
+            }
+            step(std::integral_constant<int, 0>{}, No{});
+            step(std::integral_constant<int, 1>{}, No{});
         }
         wait_loads<0>();  // the last (empty) loads still write their stages
     }
