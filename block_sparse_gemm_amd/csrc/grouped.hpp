@@ -64,62 +64,61 @@ __device__ __forceinline__ void group_rows(const int32_t* __restrict__ off, int 
     rows = max(hi - lo, 0);
 }
 
-__device__ __forceinline__ int wave_scan(int v) {  // inclusive
-    const int lane = threadIdx.x & (kWave - 1);
-#pragma unroll
-    for (int off = 1; off < kWave; off <<= 1) {
-        const int o = __shfl_up(v, off, kWave);
-        if (lane >= off) v += o;
-    }
+// Inclusive sum over the lanes: within rows of 16 lanes, then across them
+// (data-parallel moves: a shuffle through LDS would cost more than the rest
+// of the tile search).
+__device__ __forceinline__ int wave_scan(int v) {
+    v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, false);  // row_shr 1
+    v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false);  // lane 15 to rows 1, 3
+    v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false);  // lane 31 to rows 2, 3
     return v;
 }
 
-// Row tiles of all groups, H rows a tile.
+// The groups as a wave sees them, 64 at a time: lane l holds expert base + l.
+// The first 64 stay in registers between the count and the search.
 template <int H>
-__device__ __forceinline__ int row_tiles_of(const int32_t* __restrict__ off, int E, int64_t M) {
-    const int lane = threadIdx.x & (kWave - 1);
-    int n = 0;
-    for (int base = 0; base < E; base += kWave) {
-        int r0 = 0, rows = 0;
-        if (base + lane < E) group_rows(off, base + lane, M, r0, rows);
-        n += (rows + H - 1) / H;
-    }
-#pragma unroll
-    for (int o = 32; o >= 1; o >>= 1) n += __shfl_xor(n, o, kWave);
-    return __builtin_amdgcn_readfirstlane(n);
-}
+struct Groups {
+    const int32_t* off;
+    int E;
+    int64_t M;
+    int base, row0, rows, incl;  // incl: row tiles of H rows up to and with this expert's
 
-// The group of tile `tile` when every row tile of H rows has `per` tiles.
-// tile is below row_tiles_of() * per.
-template <int H>
-__device__ __forceinline__ Group group_of(const int32_t* __restrict__ off, int E, int64_t M, int per,
-                                          int tile) {
-    const int lane = threadIdx.x & (kWave - 1);
-    const int want = tile / per;  // row tile in the order of the groups
-    int before = 0;
-    Group g{0, 0, 0, 0};
-    for (int base = 0; base < E; base += kWave) {
-        int r0 = 0, rows = 0;
-        if (base + lane < E) group_rows(off, base + lane, M, r0, rows);
-        const int mine = (rows + H - 1) / H;
-        const int incl = wave_scan(mine) + before;
-        const uint64_t past = __ballot(incl > want);
-        if (past) {
-            const int at = __ffsll((unsigned long long)past) - 1;
-            g.e = base + at;
-            g.row0 = __shfl(r0, at, kWave);
-            g.rows = __shfl(rows, at, kWave);
-            g.local = tile - (__shfl(incl, at, kWave) - __shfl(mine, at, kWave)) * per;
-            break;
-        }
-        before = __shfl(incl, kWave - 1, kWave);
+    __device__ __forceinline__ void load(int b, int before) {
+        const int e = b + (threadIdx.x & (kWave - 1));
+        base = b;
+        row0 = rows = 0;
+        if (e < E) group_rows(off, e, M, row0, rows);
+        incl = wave_scan((rows + H - 1) / H) + before;
     }
-    g.e = __builtin_amdgcn_readfirstlane(g.e);
-    g.row0 = __builtin_amdgcn_readfirstlane(g.row0);
-    g.rows = __builtin_amdgcn_readfirstlane(g.rows);
-    g.local = __builtin_amdgcn_readfirstlane(g.local);
-    return g;
-}
+    __device__ __forceinline__ int last() const { return __builtin_amdgcn_readlane(incl, kWave - 1); }
+    // Row tiles of all groups; leaves the last 64 loaded.
+    __device__ __forceinline__ int count() {
+        load(0, 0);
+        for (int b = kWave; b < E; b += kWave) load(b, last());
+        return last();
+    }
+    // The group of tile `tile` when every row tile has `per` tiles; tile is
+    // below count() * per.
+    __device__ __forceinline__ Group find(int tile, int per) {
+        const int want = tile / per;  // row tile in the order of the groups
+        if (base != 0) load(0, 0);
+        uint64_t past = __ballot(incl > want);
+        while (past == 0 && base + kWave < E) {
+            load(base + kWave, last());
+            past = __ballot(incl > want);
+        }
+        const int at = past ? __ffsll((unsigned long long)past) - 1 : 0;
+        Group g;
+        g.e = base + at;
+        g.row0 = __builtin_amdgcn_readlane(row0, at);
+        g.rows = __builtin_amdgcn_readlane(rows, at);
+        g.local = tile - (__builtin_amdgcn_readlane(incl, at) - (g.rows + H - 1) / H) * per;
+        return g;
+    }
+};
 
 // -------------------------------------------------------------- operands
 
@@ -160,15 +159,22 @@ __device__ __forceinline__ u32x4 descriptor(const char* base, int64_t left) {
 // 16 bytes a lane from memory to LDS byte lds_addr + OFF + 16 lane; zeros for
 // lanes out of the descriptor's range.  Inline asm for the reason given at
 // dma16: the kernel itself waits for these loads before the barrier that
-// publishes their stage.  The s_nop covers the five wait states a descriptor
-// register needs when a vector instruction (a spilled register's restore)
-// wrote it just before.
-template <int OFF>
+// publishes their stage.  NOP: a vector instruction may have written the
+// descriptor's registers just before, which takes five wait states (four here
+// after the scalar add; the steps of the main loop set a descriptor a
+// barrier or several MFMAs ahead of its next load and need the one of m0 only).
+template <int OFF, bool NOP>
 __device__ __forceinline__ void dma16_range(uint32_t lds_addr, u32x4 desc, uint32_t off, uint32_t soff) {
-    asm volatile("s_add_u32 m0, %0, %4\n\ts_nop 3\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
-                 :
-                 : "s"(lds_addr), "v"(off), "s"(desc), "s"(soff), "n"(OFF)
-                 : "memory", "scc");
+    if constexpr (NOP)
+        asm volatile("s_add_u32 m0, %0, %4\n\ts_nop 3\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+                     :
+                     : "s"(lds_addr), "v"(off), "s"(desc), "s"(soff), "n"(OFF)
+                     : "memory", "scc");
+    else
+        asm volatile("s_add_u32 m0, %0, %4\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+                     :
+                     : "s"(lds_addr), "v"(off), "s"(desc), "s"(soff), "n"(OFF)
+                     : "memory", "scc");
 }
 
 // Wait until at most N of this wave's loads are in flight (they retire in
@@ -181,27 +187,22 @@ __device__ __forceinline__ void wait_loads() {
 
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 
-// Both 16-byte K pieces of a stage row at once: lane half h holds pieces h
-// and 2 + h of the row, for both operands alike, so every k meets itself.
-template <int DT>
-__device__ __forceinline__ void mma_stage(f32x16& acc, const u32x4* x, const u32x4* y) {
-    if constexpr (DT == kE4m3) {
-        i32x8 a, b;
+// e4m3: both 16-byte K pieces of a stage row at once.  Lane half h holds
+// pieces h and 2 + h of the row, for both operands alike, so every k meets
+// itself.
+__device__ __forceinline__ void mma_e4m3(f32x16& acc, const u32x4* x, const u32x4* y) {
+    i32x8 a, b;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            a[i] = (int)x[0][i], a[4 + i] = (int)x[1][i];
-            b[i] = (int)y[0][i], b[4 + i] = (int)y[1][i];
-        }
-        // no block scales (zero operands select the plain instruction).  It adds the products
-        // of 8 neighbouring k with 13 bits below the largest one (measured: next
-        // to a product of 1, products of 2^-13 count and of 2^-14 do not), then
-        // goes on in fp32.  The rate is twice bf16's, and 7 * 2^-13 of the sum
-        // of sizes is far below what rounding the operands to e4m3 cost.
-        acc = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, acc, 0, 0, 0, 0, 0, 0);
-    } else {
-        mma<DT>(acc, x[0], y[0]);
-        mma<DT>(acc, x[1], y[1]);
+    for (int i = 0; i < 4; ++i) {
+        a[i] = (int)x[0][i], a[4 + i] = (int)x[1][i];
+        b[i] = (int)y[0][i], b[4 + i] = (int)y[1][i];
     }
+    // no block scales (zero operands select the plain instruction).  It adds
+    // the products of 8 neighbouring k with 13 bits below the largest one
+    // (measured: next to a product of 1, products of 2^-13 count and of 2^-14
+    // do not), then goes on in fp32.  The rate is twice bf16's, and 7 * 2^-13
+    // of the sum of sizes is far below what rounding the operands to e4m3 cost.
+    acc = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, acc, 0, 0, 0, 0, 0, 0);
 }
 
 // f(0), ..., f(N - 1) with the index as a constant.
@@ -335,7 +336,7 @@ __device__ __forceinline__ void ragged_tile(char* smem, const Operand (*op)[3], 
         constexpr bool KC = i == 0 ? AK : BK, TAIL = KC && !decltype(fast)::value;
         if constexpr (HALF && pnl == 1) return;
         else
-            dma16_range<(pnl < 2 ? pnl : PA + pnl - 2) * kPanelBytes + sg * 1024>(
+            dma16_range<(pnl < 2 ? pnl : PA + pnl - 2) * kPanelBytes + sg * 1024, !decltype(fast)::value>(
                 lds_lt, desc[i], TAIL ? off[pnl][sg] | tail : off[pnl][sg], KC ? soff : 0u);
     };
     auto next_stage = [&]() {
@@ -413,7 +414,7 @@ __device__ __forceinline__ void ragged_tile(char* smem, const Operand (*op)[3], 
         constexpr bool FAST = decltype(fast)::value;
         // fragment reads, MFMA groups, and the groups the reads are spread over:
         // the last ones have no reads, so the next barrier finds them returned
-        constexpr int NR = 2 * (NMI + 4), GROUPS = NMI * 4, READ = GROUPS * 3 / 4;
+        constexpr int NR = 2 * (NMI + 4), GROUPS = NMI * 4, READ = GROUPS / 2;
         wait_loads<(STAGES - 2) * LPT>();
         __syncthreads();
         rd += STAGE_BYTES;
@@ -423,6 +424,10 @@ __device__ __forceinline__ void ragged_tile(char* smem, const Operand (*op)[3], 
 #pragma unroll
             for (int r = g * NR / READ; r < (g + 1) * NR / READ && r < NR; ++r)
                 read1(lds + rd, r & 1, r >> 1, af[c1], bf[c1]);
+            if constexpr (DT != kE4m3) {
+                mma<DT>(acc[g >> 2][g & 3], bf[c0][g & 3][0], af[c0][g >> 2][0]);
+                __builtin_amdgcn_sched_barrier(0);
+            }
             if constexpr (HALF) dma(gc, fast);
             else if constexpr (g % 2 == 0) dma(std::integral_constant<int, g / 2>{}, fast);
             if constexpr (FAST) {
@@ -436,7 +441,8 @@ __device__ __forceinline__ void ragged_tile(char* smem, const Operand (*op)[3], 
             } else {
                 if constexpr (g == GROUPS - 1) next();
             }
-            mma_stage<DT>(acc[g >> 2][g & 3], bf[c0][g & 3], af[c0][g >> 2]);
+            if constexpr (DT == kE4m3) mma_e4m3(acc[g >> 2][g & 3], bf[c0][g & 3], af[c0][g >> 2]);
+            else mma<DT>(acc[g >> 2][g & 3], bf[c0][g & 3][1], af[c0][g >> 2][1]);
             __builtin_amdgcn_sched_barrier(0);
         });
     };
@@ -610,13 +616,14 @@ __global__ __launch_bounds__(kGemmThreads, TileShape<H>::kPerCu) void grouped_ge
     __shared__ __attribute__((aligned(1024))) char smem[TileShape<H>::kLds];
     constexpr int W = DUAL ? 128 : 256;
     const int tn = (P.N + W - 1) / W;
-    const int ntiles = row_tiles_of<H>(P.row_offsets, P.E, P.M) * tn;
+    Groups<H> groups{P.row_offsets, P.E, P.M};
+    const int ntiles = groups.count() * tn;
     const int nseg = SPLIT ? P.nseg : 1;
     if ((int)blockIdx.x >= ntiles * nseg) return;
     // segment-major: what an XCD runs at once shares one K segment of its operands
     const int v = xcd_remap(blockIdx.x, ntiles * nseg);
     const int seg = SPLIT ? v / ntiles : 0;
-    const Group g = group_of<H>(P.row_offsets, P.E, P.M, tn, v - seg * ntiles);
+    const Group g = groups.find(v - seg * ntiles, tn);
     int tm, tq;
     grouped_tile(g.local, (g.rows + H - 1) / H, tn, kGroupedRows, tm, tq);
     const int mr = min(H, g.rows - H * tm);
