@@ -18,6 +18,15 @@ gradients run on a second stream, each as soon as its inputs exist (dW2 beside t
 beside the input-gradient product), so the tail of one product's grid and
 the other's fill the GPU together.
 
+With ``bin_rows = 1`` nothing is padded: the routing's bins are the ragged
+groups of grouped_gemm and grouped_wgrad, which take the place of sdd, dsd and
+dstd (and of the topology), activations are [T k, f] matrices instead of
+blocks, and f need not be a multiple of 128.  That is the form for few tokens
+(a serving batch) and for widths off the block grid.
+
+``Norm`` is what stands in front of a layer: the residual's addition and the
+root-mean-square norm, and its gradient.
+
 torch only allocates device memory and provides the stream; every step runs
 in libbsg.so.  All buffers are sized once for the worst-case routing
 (``max_padded_rows``), so a layer call never synchronises the host.
@@ -43,7 +52,8 @@ class Shape:
     yp_dtype: str = "bf16"     # storage of Yp / dXp
     renorm: bool = False
     backward: bool = False
-    bin_rows: int = 128        # expert bins padded to a multiple of this (64, 128 or 256)
+    bin_rows: int = 128        # expert bins padded to a multiple of this (64, 128 or 256),
+                               # or 1: ragged groups, nothing padded
 
     @classmethod
     def of(cls, cfg) -> "Shape":
@@ -83,6 +93,10 @@ class Layer:
         # y, and Yp when a backward follows; backward with GeLU experts: dx
         # straight from the product, no dXp)
         self.fuse_top1 = s.k == 1 and s.dtype == "bf16" and s.yp_tdtype == torch.bfloat16
+        # the ragged products write assignment rows, and run in order
+        self.ragged = s.bin_rows == 1
+        if self.ragged:
+            self.fuse_top1 = self.overlap = False
         dev = torch.device(device)
         # plain DSDs whose tiles walk at least 32 K-blocks (f >= 4096, or the
         # SwiGLU backward's two block sets) split their last, partly filled
@@ -90,16 +104,32 @@ class Layer:
         F = s.f // bsg.BLOCK
         long_k = F >= 32 or (s.act == "swiglu" and s.backward and 2 * F >= 32)
         self.dsd_ws = torch.empty(bsg.dsd_workspace_bytes() // 4, dtype=torch.float32,
-                                  device=dev) if long_k and not self.fuse_top1 else None
+                                  device=dev) \
+            if long_k and not self.fuse_top1 and not self.ragged else None
         i32 = dict(dtype=torch.int32, device=dev)
         A = s.T * s.k
         self.Tp_max = bsg.max_padded_rows(s.T, s.k, s.E, s.bin_rows)
         # bins of 64 rows need blocks of 64 rows (a block holds one expert's rows)
         self.block_rows = 64 if s.bin_rows == 64 else bsg.BLOCK
-        self.topo = bsg.Topology(self.Tp_max, s.E, s.f, device=dev, block_rows=self.block_rows)
-        nnz_max = self.topo.nnz_max
-        br = self.block_rows
         dt, ydt = s.tdtype, s.yp_tdtype
+        planes = 2 if s.act == "swiglu" else 1
+        if self.ragged:
+            self.topo = None
+            kept = (planes, A, s.f) if planes == 2 else (A, s.f)
+            self.act = torch.zeros(A, s.f, dtype=dt, device=dev)
+            epi = "silu_mul" if planes == 2 else "gelu"
+            need = [bsg.grouped_gemm_workspace_bytes(A, s.d, s.f, s.E, epi),
+                    bsg.grouped_gemm_workspace_bytes(A, s.f, s.d, s.E)]
+            if s.backward:
+                need.append(bsg.grouped_gemm_workspace_bytes(A, s.d, s.f, s.E, epi + "_bwd"))
+            self.ragged_ws = torch.empty(max(need), dtype=torch.uint8, device=dev) \
+                if max(need) else None
+        else:
+            self.topo = bsg.Topology(self.Tp_max, s.E, s.f, device=dev,
+                                     block_rows=self.block_rows)
+            blocks = self.topo.nnz_max * self.block_rows
+            kept = (planes * blocks, bsg.BLOCK)
+            self.act = torch.zeros(blocks, bsg.BLOCK, dtype=dt, device=dev)
         self.expert_idx = torch.zeros(A, **i32)
         self.gate = torch.zeros(A, dtype=torch.float32, device=dev)
         self.dest_row = torch.zeros(A, **i32)
@@ -109,14 +139,12 @@ class Layer:
                                     dtype=torch.uint8, device=dev)
         self.row_src = torch.zeros(self.Tp_max, **i32)
         self.xp = torch.zeros(self.Tp_max, s.d, dtype=dt, device=dev)
-        self.act = torch.zeros(nnz_max * br, bsg.BLOCK, dtype=dt, device=dev)
-        # what the backward keeps of the forward, block-major like A: GeLU'(h),
+        # what the backward keeps of the forward, laid out like A: GeLU'(h),
         # or for SwiGLU two planes, silu(g) then u * silu'(g)
-        planes = 2 if s.act == "swiglu" else 1
-        self.gp = torch.zeros(planes * nnz_max * br, bsg.BLOCK, dtype=dt, device=dev) \
-            if s.backward else None
+        self.gp = torch.zeros(kept, dtype=dt, device=dev) if s.backward else None
         self.yp = torch.zeros(self.Tp_max, s.d, dtype=ydt, device=dev)
         self.y = torch.zeros(s.T, s.d, dtype=dt, device=dev)
+        self.clip_ws = self.grad_norm = None
         if s.backward:
             self.dyp = torch.zeros(self.Tp_max, s.d, dtype=dt, device=dev)
             self.row_src_b = torch.zeros(self.Tp_max, **i32)
@@ -151,6 +179,16 @@ class Layer:
         c("route_permute_topology", bsg.route_permute_topology, logits, s.k, s.renorm, self.expert_idx, self.gate,
           self.dest_row, self.counts, self.bin_offsets, self.route_ws, x, self.Tp_max,
           self.row_src, self.xp, s.f, t, bin_rows=s.bin_rows)
+        if self.ragged:
+            sw = s.act == "swiglu"
+            c("grouped_up", bsg.grouped_gemm, self.xp, self.bin_offsets, self.up_by_expert(W1),
+              self.act, "silu_mul" if sw else "gelu", b2=self.up_by_expert(W3) if sw else None,
+              aux_out=self.gp, workspace=self.ragged_ws)
+            c("grouped_down", bsg.grouped_gemm, self.act, self.bin_offsets, self.down_by_expert(W2),
+              self.yp, workspace=self.ragged_ws)
+            c("unpermute_combine", bsg.unpermute_combine, self.yp, self.dest_row, self.gate, s.T,
+              s.k, s.d, self.y)
+            return self.y
         if s.act == "swiglu":
             c("sdd", bsg.sdd, self.xp, W1, s.d, t, "silu_mul", self.act, b2=W3, aux_out=self.gp)
         else:
@@ -166,6 +204,14 @@ class Layer:
           s.k, s.d, self.y)
         return self.y
 
+    def up_by_expert(self, W):
+        """W1 or W3 [d, E f] as [E, d, f] (a view)."""
+        return W.view(self.s.d, self.s.E, self.s.f).permute(1, 0, 2)
+
+    def down_by_expert(self, W):
+        """W2 [E f, d] as [E, f, d] (a view)."""
+        return W.view(self.s.E, self.s.f, self.s.d)
+
     def plane(self, blocks, i):
         """Plane i of a two-plane block array (a view)."""
         n = self.topo.nnz_max * self.block_rows
@@ -176,6 +222,8 @@ class Layer:
         c = self._call
         main = torch.cuda.current_stream()
         sw = s.act == "swiglu"
+        if self.ragged:
+            return self._backward_ragged(dy, W1, W2, W3)
         dh0 = self.plane(self.dh, 0) if sw else self.dh
 
         def sdd_bwd():
@@ -228,6 +276,40 @@ class Layer:
         main.wait_event(self.ev_wgrad)  # the step ends when both streams have
         return self.grads()
 
+    def _backward_ragged(self, dy, W1, W2, W3):
+        s, c, off, ws = self.s, self._call, self.bin_offsets, self.ragged_ws
+        sw = s.act == "swiglu"
+        c("permute_pad_gate_bwd", bsg.permute_pad_gate_backward, dy, s.k, self.dest_row,
+          self.gate, self.counts, off, s.E, self.Tp_max, self.row_src_b, self.dyp, self.logits,
+          s.renorm, self.expert_idx, self.yp, self.dlogits, bin_rows=1)
+        c("grouped_up_bwd", bsg.grouped_gemm, self.dyp, off, self.down_by_expert(W2), self.dh,
+          "silu_mul_bwd" if sw else "gelu_bwd", trans_b=True, aux_in=self.gp, workspace=ws)
+        dh = [self.dh[0], self.dh[1]] if sw else [self.dh]
+        c("grouped_down_bwd", bsg.grouped_gemm, dh[0], off, self.up_by_expert(W1), self.dxp,
+          trans_b=True, a2=dh[1] if sw else None, b2=self.up_by_expert(W3) if sw else None,
+          workspace=ws)
+        c("unpermute_combine_bwd", bsg.unpermute_combine, self.dxp, self.dest_row, None, s.T,
+          s.k, s.d, self.dx)
+        c("grouped_dw2", bsg.grouped_wgrad, self.act, self.dyp, off, self.down_by_expert(self.dW2))
+        c("grouped_dw1", bsg.grouped_wgrad, self.xp, dh[0], off, self.up_by_expert(self.dW1))
+        if sw:
+            c("grouped_dw3", bsg.grouped_wgrad, self.xp, dh[1], off, self.up_by_expert(self.dW3))
+        return self.grads()
+
+    def clip_grads(self, max_norm, more=()):
+        """Scale the weight gradients, together with the gradients in ``more``
+        (a router's, a norm's), in place to a joint 2-norm of at most
+        max_norm; returns the norm before (one fp32 on the device)."""
+        grads = [*self.grads()[1:], *more]
+        if self.clip_ws is None:
+            dev = self.dW1.device
+            self.clip_ws = torch.empty(bsg.grad_norm_workspace_bytes(), dtype=torch.uint8,
+                                       device=dev)
+            self.grad_norm = torch.zeros((), dtype=torch.float32, device=dev)
+        self._call("grad_norm", bsg.grad_norm, grads, self.grad_norm, self.clip_ws)
+        self._call("grad_clip", bsg.grad_clip, grads, self.grad_norm, max_norm)
+        return self.grad_norm
+
     def grads(self):
         """(dx, dW1, dW2), plus dW3 for SwiGLU experts."""
         g = (self.dx, self.dW1, self.dW2)
@@ -249,6 +331,40 @@ class Layer:
         base = (r // br) * F
         out = [b[base + j, r % br] for j in range(F)]
         return torch.cat(out, dim=1)
+
+
+class Norm:
+    """The root-mean-square norm in front of a layer, with preallocated
+    buffers: ``forward`` adds the residual stream (h = x + residual) and
+    normalises the sum, in x's type or, with ``e4m3``, in 8 bits with one
+    scale a row; ``backward`` gives the gradient of both addends and of the
+    weight."""
+
+    def __init__(self, T: int, d: int, weight: torch.Tensor, eps: float = 1e-5, residual=True,
+                 e4m3=False, backward=False):
+        dt, dev = weight.dtype, weight.device
+        self.weight, self.eps = weight, eps
+        self.h = torch.zeros(T, d, dtype=dt, device=dev) if residual else None
+        self.y = torch.zeros(T, d, dtype=torch.float8_e4m3fn if e4m3 else dt, device=dev)
+        self.y_scale = torch.zeros(T, dtype=torch.float32, device=dev) if e4m3 else None
+        self.rstd = torch.zeros(T, dtype=torch.float32, device=dev)
+        if backward:
+            self.dx = torch.zeros(T, d, dtype=dt, device=dev)
+            self.dweight = torch.zeros(d, dtype=torch.float32, device=dev)
+            self.ws = torch.empty(bsg.rms_norm_backward_workspace_bytes(T, d), dtype=torch.uint8,
+                                  device=dev)
+
+    def forward(self, x, residual=None):
+        bsg.rms_norm(x, self.weight, self.eps, self.y, h=self.h, residual=residual,
+                     y_scale=self.y_scale, rstd=self.rstd)
+        self.stored = x if residual is None else self.h
+        return self.y
+
+    def backward(self, dy, dh=None):
+        """(dx, dweight); dh: the gradient that reaches h along the residual stream."""
+        bsg.rms_norm_backward(dy, self.stored, self.weight, self.rstd, self.dx, self.dweight,
+                              self.ws, dh=dh)
+        return self.dx, self.dweight
 
 
 def from_numpy(t, dtype_str: str, device="cuda") -> torch.Tensor:
