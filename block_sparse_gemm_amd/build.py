@@ -19,7 +19,7 @@ LIB = os.path.join(HERE, "libbsg.so")
 
 SOURCES = ["gemm_br128.hip", "gemm_br64.hip", "route.hip", "movement.hip", "topology.hip",
            "gemm.hip", "grouped_bf16.hip", "grouped_f32.hip", "grouped_e4m3.hip", "grouped.hip",
-           "norm.hip", "clip.hip", "api.cpp", "api_ops.cpp"]
+           "grouped_plan.cpp", "norm.hip", "clip.hip", "api.cpp", "api_ops.cpp"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 
