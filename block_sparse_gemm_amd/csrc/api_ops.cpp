@@ -145,9 +145,9 @@ static bool grouped_ld_fits(int64_t ld, int es, bool k_contiguous) {
 
 static int grouped_elt_bytes(int dtype) { return dtype == BSG_E4M3 ? 1 : elt_bytes(dtype); }
 
-// Compute units that the split along K is planned for (an MI355X's: the size
+// Compute units that tiles and segments are planned for (an MI355X's: the size
 // query has no stream to ask).
-constexpr int kSegmentCus = 256;
+constexpr int kPlanCus = 256;
 
 size_t bsg_grouped_gemm_workspace_bytes(int64_t M, int K, int N, int E, int epilogue) {
     if (M < 0 || M > INT32_MAX || K < 1 || K > kMaxWidth || N < 1 || N > kMaxWidth || E < 1 ||
@@ -157,7 +157,7 @@ size_t bsg_grouped_gemm_workspace_bytes(int64_t M, int K, int N, int E, int epil
     // the most segments that any type has on a device of this many compute units
     int n = 1;
     for (const int dtype : {BSG_F32, BSG_BF16, BSG_E4M3})
-        n = std::max(n, bsg::grouped_segments(M, K, N, E, epilogue, dtype, kSegmentCus));
+        n = std::max(n, bsg::grouped_plan(M, K, N, E, epilogue, dtype, kPlanCus, bsg::kMaxSegments).segments);
     return n == 1 ? 0 : (size_t)n * M * N * (epilogue == BSG_EPI_SILU_MUL ? 2 : 1) * sizeof(float);
 }
 
@@ -245,13 +245,12 @@ bsg_status bsg_grouped_gemm(const void* a, const void* a2, int64_t lda, const fl
     p.aux_out = aux_out;
     // segments as many as planned, or as the workspace holds
     const int64_t share = M * N * (epilogue == BSG_EPI_SILU_MUL ? 2 : 1) * (int64_t)sizeof(float);
-    p.nseg = 1;
-    if (workspace && (int64_t)(workspace_bytes / 2) >= share)
-        p.nseg = (int)std::min<int64_t>(
-            bsg::grouped_segments(M, K, N, E, epilogue, dtype, kSegmentCus),
-            (int64_t)workspace_bytes / share);
+    const int64_t fit = workspace ? (int64_t)std::min<size_t>(workspace_bytes, INT64_MAX) / share : 1;
+    const bsg::GroupedPlan plan = bsg::grouped_plan(M, K, N, E, epilogue, dtype, kPlanCus, fit);
     p.ws = (float*)workspace;
-    p.tile_rows = bsg::grouped_tile_rows(M, E, K, N, epilogue, dtype, kSegmentCus);
+    p.nseg = plan.segments;
+    p.tile_rows = plan.rows;
+    p.tile_cols = plan.cols;
     p.lda = lda;
     p.ldb = ldb;
     p.ldc = ldc;
@@ -294,7 +293,7 @@ bsg_status bsg_grouped_wgrad(const void* a, int64_t lda, const void* dmat, int64
         REQUIRE_VEC_PTR(a);
         REQUIRE_VEC_PTR(dmat);
     }
-    if ((int64_t)E * ((K + 255) / 256) * ((N + 255) / 256) > INT32_MAX)
+    if ((int64_t)E * ((K + 127) / 128) * ((N + 127) / 128) > INT32_MAX)
         return fail(BSG_EUNSUPPORTED, "too many tiles");
     bsg::GroupedParams p{};
     p.a = a;
@@ -309,6 +308,9 @@ bsg_status bsg_grouped_wgrad(const void* a, int64_t lda, const void* dmat, int64
     p.K = K;
     p.N = N;
     p.E = E;
+    const bsg::GroupedPlan plan = bsg::grouped_wgrad_plan(M, K, N, E, dtype, kPlanCus);
+    p.tile_rows = plan.rows;
+    p.tile_cols = plan.cols;
     return hip_status(bsg::launch_grouped_wgrad(p, c_dtype, dtype, (hipStream_t)stream),
                       "grouped_wgrad");
 }

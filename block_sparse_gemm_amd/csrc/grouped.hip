@@ -3,20 +3,18 @@
 
 namespace bsg {
 
-template <int DT, int OUT, int H>
-static hipError_t wgrad_h(const GroupedParams& p, hipStream_t s) {
-    const int64_t grid = (int64_t)p.E * ((p.K + H - 1) / H) * ((p.N + 255) / 256);
-    hipLaunchKernelGGL((grouped_wgrad_kernel<DT, OUT, H>), dim3((unsigned)grid), dim3(kGemmThreads), 0,
-                       s, p);
+template <int DT, int OUT, int H, int W>
+static hipError_t wgrad_tile(const GroupedParams& p, hipStream_t s) {
+    const int64_t grid = (int64_t)p.E * ((p.K + H - 1) / H) * ((p.N + W - 1) / W);
+    hipLaunchKernelGGL((grouped_wgrad_kernel<DT, OUT, H, W>), dim3((unsigned)grid), dim3(kGemmThreads),
+                       0, s, p);
     return hipGetLastError();
 }
 
 template <int DT, int OUT>
 static hipError_t wgrad_go(const GroupedParams& p, hipStream_t s) {
-    // Short sums (few rows an expert) run two workgroups a compute unit.
-    // Measured, 128 / 256 rows a tile: 64 experts of 256 rows 53 / 62 us, of
-    // 2048 rows 1099 / 1071 us.
-    return p.M / p.E <= 512 ? wgrad_h<DT, OUT, 128>(p, s) : wgrad_h<DT, OUT, 256>(p, s);
+    if (p.tile_cols == 128) return wgrad_tile<DT, OUT, 128, 128>(p, s);
+    return p.tile_rows == 128 ? wgrad_tile<DT, OUT, 128, 256>(p, s) : wgrad_tile<DT, OUT, 256, 256>(p, s);
 }
 
 hipError_t launch_grouped_wgrad(const GroupedParams& p, int c_dtype, int dtype, hipStream_t s) {

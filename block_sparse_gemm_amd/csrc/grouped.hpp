@@ -244,6 +244,13 @@ __device__ __forceinline__ void epilogue4(float* v, const float* u, float* x, fl
     }
 }
 
+__device__ __forceinline__ void unpack4(u32x2 u, float* f) {  // four bf16
+    f[0] = __uint_as_float(u[0] << 16);
+    f[1] = __uint_as_float(u[0] & 0xffff0000u);
+    f[2] = __uint_as_float(u[1] << 16);
+    f[3] = __uint_as_float(u[1] & 0xffff0000u);
+}
+
 // Whether the epilogue has a second and a third output.
 template <int EPI>
 constexpr bool kHasX = EPI == kEpiGeluSave || EPI == kEpiSiluMulSave || EPI == kEpiSiluMulBwd;
@@ -268,21 +275,23 @@ struct TileOut {
     int mr, n0, N;
 };
 
-// AK, BK: operand K-contiguous.  HALF: at most 128 rows (waves split them 64
-// by 64 and the second A panel is not loaded).  K of one set; sets 2: a second
-// pair of operands into the same accumulators.  op: A, B (DUAL: its second
-// panel's B) of the first set, then of the second.
-// STAGES K-tiles in the ring, of 32 KB each (HALF: 24 KB).
-// SPLIT: the sums of a K segment go to o.part instead of the epilogue.
-template <int DT, bool AK, bool BK, int EPI, int OUT, bool HALF, int STAGES, bool SPLIT>
+// AK, BK: operand K-contiguous.  PA, PB: panels of A and of B, 1 or 2: the
+// tile is 128 PA rows x 128 PB columns, two by two waves of 64 PA x 64 PB
+// (DUAL: PB = 2, one panel of each product's B, the tile 128 columns wide).  K
+// of one set; sets 2: a second pair of operands into the same accumulators.
+// op: A, B (DUAL: its second panel's B) of the first set, then of the second.
+// STAGES K-tiles in the ring, of 8 KB a panel.  SPLIT: the sums of a K segment
+// go to o.part instead of the epilogue.
+template <int DT, bool AK, bool BK, int EPI, int OUT, int PA, int PB, int STAGES, bool SPLIT>
 __device__ __forceinline__ void ragged_tile(char* smem, const Operand (*op)[3], int64_t lda_b,
                                              int64_t ldb_b, int64_t K, int sets, const TileOut& o) {
     constexpr int ES = GElt<DT>::kBytes, KT = GElt<DT>::kKt;
     constexpr bool DUAL = EPI == kEpiSiluMul || EPI == kEpiSiluMulSave;
-    constexpr int LPT = HALF ? kLoadsPerTile - 2 : kLoadsPerTile;
-    constexpr int NMI = HALF ? 2 : 4, NI = DUAL ? 2 : 4;
-    constexpr int PA = HALF ? 1 : 2;  // A panels; B's two follow them in a stage
-    constexpr int STAGE_BYTES = (PA + 2) * kPanelBytes;
+    constexpr int LPT = kSegsPerWave * (PA + PB);  // direct loads per wave and K-tile
+    constexpr int NMI = 2 * PA, NNI = 2 * PB;      // 32 x 32 accumulators of a wave
+    constexpr int NI = DUAL ? 2 : NNI;             // those of one product, along N
+    constexpr int STAGE_BYTES = (PA + PB) * kPanelBytes;
+    static_assert(!DUAL || PB == 2, "a panel for each product");
     static_assert(DT != kE4m3 || (AK && BK), "e4m3 operands are K-contiguous");
     lds_t* lds = (lds_t*)smem;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -293,8 +302,8 @@ __device__ __forceinline__ void ragged_tile(char* smem, const Operand (*op)[3], 
 
     const int nk1 = (int)((K + KT - 1) / KT), nk = nk1 * sets;
 
-    // ---- loads: K-tile `lt` is next to go out.  Panels 0, 1: A; 2, 3: B.
-    // The second panel of an operand is the first one's descriptor with
+    // ---- loads: K-tile `lt` is next to go out.  A's panels, then B's.  The
+    // second panel of an operand is the first one's descriptor with
     // larger lane offsets.  K-contiguous operands advance through the scalar
     // offset under a constant descriptor; the others move their base.
     constexpr int NOP = DUAL ? 3 : 2;
@@ -329,15 +338,14 @@ __device__ __forceinline__ void ragged_tile(char* smem, const Operand (*op)[3], 
     uint32_t tail = nk1 == 1 ? behind : 0u;   // `behind` while K-tile lt is a set's last
     const uint32_t lds0 = lds_u32(lds) + wave * kSegsPerWave * 1024;
     uint32_t lds_lt = lds0;                   // this wave's segments in K-tile lt's stage
-    // load j (0..7): panel j & 3, segment j >> 2; FAST: not a set's last K-tile
+    // load j (0 .. LPT - 1); FAST: not a set's last K-tile
     auto dma = [&](auto jc, auto fast) {
-        constexpr int j = decltype(jc)::value, pnl = j & 3, sg = j >> 2;
-        constexpr int i = pnl < 2 ? 0 : DUAL && pnl == 3 ? 2 : 1;
+        constexpr int j = decltype(jc)::value, pnl = j % (PA + PB), sg = j / (PA + PB);
+        constexpr int lane_off = pnl < PA ? pnl : 2 + pnl - PA;
+        constexpr int i = pnl < PA ? 0 : DUAL && pnl == PA + 1 ? 2 : 1;
         constexpr bool KC = i == 0 ? AK : BK, TAIL = KC && !decltype(fast)::value;
-        if constexpr (HALF && pnl == 1) return;
-        else
-            dma16_range<(pnl < 2 ? pnl : PA + pnl - 2) * kPanelBytes + sg * 1024, !decltype(fast)::value>(
-                lds_lt, desc[i], TAIL ? off[pnl][sg] | tail : off[pnl][sg], KC ? soff : 0u);
+        dma16_range<pnl * kPanelBytes + sg * 1024, !decltype(fast)::value>(
+            lds_lt, desc[i], TAIL ? off[lane_off][sg] | tail : off[lane_off][sg], KC ? soff : 0u);
     };
     auto next_stage = [&]() {
         ++lt;
@@ -380,27 +388,27 @@ __device__ __forceinline__ void ragged_tile(char* smem, const Operand (*op)[3], 
         }
     };
 
-    f32x16 acc[NMI][4];
+    f32x16 acc[NMI][NNI];
 #pragma unroll
     for (int i = 0; i < NMI; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+        for (int j = 0; j < NNI; ++j)
 #pragma unroll
             for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
 
-    // fragment f (0..NMI-1: A, then four of B), K piece c of the K-tile in stage st
+    // fragment f (0..NMI-1: A, then B's), K piece c of the K-tile in stage st
     auto read1 = [&](const lds_t* st, int c, int f, u32x4 (*af)[2], u32x4 (*bf)[2]) {
         if (f < NMI) {
-            af[f][c] = HALF ? frag<LT, AK>(st, 64 * wm + 32 * f, c)
-                            : frag<LT, AK>(st + wm * kPanelBytes, 32 * f, c);
+            af[f][c] = PA == 1 ? frag<LT, AK>(st, 64 * wm + 32 * f, c)
+                               : frag<LT, AK>(st + wm * kPanelBytes, 32 * f, c);
         } else {
             const int ni = f - NMI;
-            const int pnl = PA + (DUAL ? ni >> 1 : wn);
-            const int row = DUAL ? wn * 64 + 32 * (ni & 1) : 32 * ni;
+            const int pnl = PA + (DUAL ? ni >> 1 : PB == 1 ? 0 : wn);
+            const int row = DUAL ? wn * 64 + 32 * (ni & 1) : PB == 1 ? wn * 64 + 32 * ni : 32 * ni;
             bf[ni][c] = frag<LT, BK>(st + pnl * kPanelBytes, row, c);
         }
     };
-    u32x4 af[2][NMI][2], bf[2][4][2];
+    u32x4 af[2][NMI][2], bf[2][NNI][2];
     int rd = 0;  // byte of the stage that the next step reads
     // One K-tile: its MFMAs, and among them the fragment reads of the next
     // one (published by the barrier before) and the loads STAGES ahead into
@@ -414,7 +422,9 @@ __device__ __forceinline__ void ragged_tile(char* smem, const Operand (*op)[3], 
         constexpr bool FAST = decltype(fast)::value;
         // fragment reads, MFMA groups, and the groups the reads are spread over:
         // the last ones have no reads, so the next barrier finds them returned
-        constexpr int NR = 2 * (NMI + 4), GROUPS = NMI * 4, READ = GROUPS / 2;
+        constexpr int NR = 2 * (NMI + NNI), GROUPS = NMI * NNI, READ = GROUPS / 2;
+        // the group behind the last load of A (its second segments go out first)
+        constexpr int A_OUT = ((PA + PB + PA) * GROUPS - 1) / LPT;
         wait_loads<(STAGES - 2) * LPT>();
         __syncthreads();
         rd += STAGE_BYTES;
@@ -424,15 +434,17 @@ __device__ __forceinline__ void ragged_tile(char* smem, const Operand (*op)[3], 
 #pragma unroll
             for (int r = g * NR / READ; r < (g + 1) * NR / READ && r < NR; ++r)
                 read1(lds + rd, r & 1, r >> 1, af[c1], bf[c1]);
+            constexpr int mi = g / NNI, ni = g % NNI;
             if constexpr (DT != kE4m3) {
-                mma<DT>(acc[g >> 2][g & 3], bf[c0][g & 3][0], af[c0][g >> 2][0]);
+                mma<DT>(acc[mi][ni], bf[c0][ni][0], af[c0][mi][0]);
                 __builtin_amdgcn_sched_barrier(0);
             }
-            if constexpr (HALF) dma(gc, fast);
-            else if constexpr (g % 2 == 0) dma(std::integral_constant<int, g / 2>{}, fast);
+            constexpr int j0 = g * LPT / GROUPS, j1 = (g + 1) * LPT / GROUPS;
+            unroll<j1 - j0>([&](auto jc) {
+                dma(std::integral_constant<int, j0 + decltype(jc)::value>{}, fast);
+            });
             if constexpr (FAST) {
-                // behind the last load of A, and of B
-                if constexpr (g == (HALF ? 5 : 11)) advance(0, 1);
+                if constexpr (g == A_OUT) advance(0, 1);
                 if constexpr (g == GROUPS - 1) {
                     advance(1, NOP);
                     soff += kRowBytes;
@@ -441,8 +453,8 @@ __device__ __forceinline__ void ragged_tile(char* smem, const Operand (*op)[3], 
             } else {
                 if constexpr (g == GROUPS - 1) next();
             }
-            if constexpr (DT == kE4m3) mma_e4m3(acc[g >> 2][g & 3], bf[c0][g & 3], af[c0][g >> 2]);
-            else mma<DT>(acc[g >> 2][g & 3], bf[c0][g & 3][1], af[c0][g >> 2][1]);
+            if constexpr (DT == kE4m3) mma_e4m3(acc[mi][ni], bf[c0][ni], af[c0][mi]);
+            else mma<DT>(acc[mi][ni], bf[c0][ni][1], af[c0][mi][1]);
             __builtin_amdgcn_sched_barrier(0);
         });
     };
@@ -450,13 +462,13 @@ __device__ __forceinline__ void ragged_tile(char* smem, const Operand (*op)[3], 
         using No = std::false_type;
         using Yes = std::true_type;
         for (int t = 0; t < STAGES; ++t) {
-            unroll<kLoadsPerTile>([&](auto jc) { dma(jc, No{}); });
+            unroll<LPT>([&](auto jc) { dma(jc, No{}); });
             next();
         }
         wait_loads<(STAGES - 1) * LPT>();
         __syncthreads();
 #pragma unroll
-        for (int f = 0; f < NMI + 4; ++f) {
+        for (int f = 0; f < NMI + NNI; ++f) {
             read1(lds, 0, f, af[0], bf[0]);
             read1(lds, 1, f, af[0], bf[0]);
         }
@@ -473,15 +485,15 @@ __device__ __forceinline__ void ragged_tile(char* smem, const Operand (*op)[3], 
         wait_loads<0>();  // the last (empty) loads still write their stages
     }
 
-    const int wcol = o.n0 + wn * (DUAL ? 64 : 128);  // the wave's first column
+    const int wcol = o.n0 + wn * 32 * NI;  // the wave's first column
 
     // ---- a K segment: fp32 sums as they are, for the launch that adds them
     if constexpr (SPLIT) {
 #pragma unroll
         for (int mi = 0; mi < NMI; ++mi) {
-            const int row = (HALF ? 64 : 128) * wm + 32 * mi + l32;
+            const int row = 64 * PA * wm + 32 * mi + l32;
 #pragma unroll
-            for (int ni = 0; ni < 4; ++ni)
+            for (int ni = 0; ni < NNI; ++ni)
 #pragma unroll
                 for (int g = 0; g < 4; ++g) {
                     const int col = wcol + 32 * (DUAL ? ni & 1 : ni) + 8 * g + 4 * lh;
@@ -496,13 +508,13 @@ __device__ __forceinline__ void ragged_tile(char* smem, const Operand (*op)[3], 
     }
 
     // ---- epilogue: bf16 results go through LDS, 32 rows at a time, so that
-    // stores write whole rows of 256 (DUAL: 128) bytes; fp32 results are
+    // stores write whole rows of 256 (a wave of 64 columns: 128) bytes; fp32 results are
     // stored from the accumulators.  Chunk c of staged row r lies at slot
     // c ^ (r & MASK), which spreads both the writes and the reads over all
     // banks.
     constexpr bool STAGE = OUT == kBf16;
     constexpr int OES = OUT == kBf16 ? 2 : 4;
-    constexpr int ROWB = DUAL ? 128 : 256;  // bytes of a staged row
+    constexpr int ROWB = 64 * NI;  // bytes of a staged row
     constexpr int MASK = ROWB / 16 - 1;
     if constexpr (STAGE) __syncthreads();  // the operand ring is free
     static_assert(4 * (DUAL ? 3 : 2) * 32 * ROWB <= STAGES * STAGE_BYTES, "staging fits the ring");
@@ -526,60 +538,86 @@ __device__ __forceinline__ void ragged_tile(char* smem, const Operand (*op)[3], 
                 __builtin_nontemporal_store(u, (u32x4*)(base + ((int64_t)(trow + row) * o.ldc + col) * 2));
         }
     };
+    // e4m3: the scales of this lane's rows and columns, all loads in flight at once
+    float sa[DT == kE4m3 ? NMI : 1];
+    f32x4 sb[DT == kE4m3 ? NI : 1][4], sb2[DT == kE4m3 && DUAL ? NI : 1][4];
+    if constexpr (DT == kE4m3) {
+#pragma unroll
+        for (int mi = 0; mi < NMI; ++mi) {
+            const int row = 64 * PA * wm + 32 * mi + l32;
+            sa[mi] = row < o.mr ? o.a_scale[row] : 0.0f;
+        }
+#pragma unroll
+        for (int ni = 0; ni < NI; ++ni)
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                const int col = wcol + 32 * ni + 8 * g + 4 * lh;
+                const f32x4 zero{0, 0, 0, 0};
+                sb[ni][g] = col < o.N ? *(const f32x4*)(o.b_scale + col) : zero;
+                if constexpr (DUAL) sb2[ni][g] = col < o.N ? *(const f32x4*)(o.b2_scale + col) : zero;
+            }
+    }
+    constexpr bool ONE_IN = EPI == kEpiGeluBwd || EPI == kEpiSiluMulBwd, TWO_IN = EPI == kEpiSiluMulBwd;
+    constexpr bool SLAB_IN = ONE_IN && STAGE;  // bf16: a slab's saved factors are read ahead of it
 #pragma unroll
     for (int mi = 0; mi < NMI; ++mi) {
-        const int trow = (HALF ? 64 : 128) * wm + 32 * mi;  // the slab's first row in the tile
+        const int trow = 64 * PA * wm + 32 * mi;  // the slab's first row in the tile
         if (trow >= o.mr) break;
-        {
-            const int row = trow + l32;
-            const bool rin = row < o.mr;
-            float sa = 1.0f;
-            if constexpr (DT == kE4m3) sa = rin ? o.a_scale[row] : 0.0f;
+        const int row = trow + l32;
+        const bool rin = row < o.mr;
+        u32x2 in1[SLAB_IN ? NI : 1][4], in2[SLAB_IN && TWO_IN ? NI : 1][4];
+        if constexpr (SLAB_IN) {
 #pragma unroll
-            for (int ni = 0; ni < NI; ++ni) {
+            for (int ni = 0; ni < NI; ++ni)
 #pragma unroll
                 for (int g = 0; g < 4; ++g) {
                     const int col = wcol + 32 * ni + 8 * g + 4 * lh;
+                    const int64_t at = ((int64_t)row * o.ldc + col) * 2;
                     const bool in = rin && col < o.N;
-                    const int64_t at = ((int64_t)row * o.ldc + col) * OES;
-                    float v[4], u[4];
+                    in1[ni][g] = in ? *(const u32x2*)(o.aux_in + at) : u32x2{0, 0};
+                    if constexpr (TWO_IN) in2[ni][g] = in ? *(const u32x2*)(o.aux_in2 + at) : u32x2{0, 0};
+                }
+        }
 #pragma unroll
-                    for (int s = 0; s < 4; ++s) {
-                        v[s] = acc[mi][ni][4 * g + s];
-                        if constexpr (DUAL) u[s] = acc[mi][ni + 2][4 * g + s];
-                    }
+        for (int ni = 0; ni < NI; ++ni) {
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                const int col = wcol + 32 * ni + 8 * g + 4 * lh;
+                const bool in = rin && col < o.N;
+                const int64_t at = ((int64_t)row * o.ldc + col) * OES;
+                float v[4], u[4];
+#pragma unroll
+                for (int s = 0; s < 4; ++s) {
+                    v[s] = acc[mi][ni][4 * g + s];
+                    if constexpr (DUAL) u[s] = acc[mi][ni + 2][4 * g + s];
                     if constexpr (DT == kE4m3) {
-                        const f32x4 sb = col < o.N ? *(const f32x4*)(o.b_scale + col) : f32x4{0, 0, 0, 0};
-#pragma unroll
-                        for (int s = 0; s < 4; ++s) v[s] *= sa * sb[s];
-                        if constexpr (DUAL) {
-                            const f32x4 s2 =
-                                col < o.N ? *(const f32x4*)(o.b2_scale + col) : f32x4{0, 0, 0, 0};
-#pragma unroll
-                            for (int s = 0; s < 4; ++s) u[s] *= sa * s2[s];
-                        }
-                    }
-                    float x[4], y[4], d[4] = {0, 0, 0, 0}, q[4] = {0, 0, 0, 0};
-                    if constexpr (EPI == kEpiGeluBwd || EPI == kEpiSiluMulBwd) {
-                        if (in) load4<OUT>(o.aux_in + at, d);
-                    }
-                    if constexpr (EPI == kEpiSiluMulBwd) {
-                        if (in) load4<OUT>(o.aux_in2 + at, q);
-                    }
-                    epilogue4<EPI>(v, u, x, y, d, q);
-                    constexpr bool X = kHasX<EPI>, Y = kHasY<EPI>;
-                    if constexpr (STAGE) {
-                        put(0, 4 * ni + g, v);
-                        if constexpr (X) put(1, 4 * ni + g, x);
-                        if constexpr (Y) put(2, 4 * ni + g, y);
-                    } else if (in) {
-                        store4<OUT>(o.out + at, v);
-                        if constexpr (X) store4<OUT>((EPI == kEpiSiluMulBwd ? o.out2 : o.aux_out) + at, x);
-                        if constexpr (Y) store4<OUT>(o.aux_out2 + at, y);
+                        v[s] *= sa[mi] * sb[ni][g][s];
+                        if constexpr (DUAL) u[s] *= sa[mi] * sb2[ni][g][s];
                     }
                 }
-                __builtin_amdgcn_sched_barrier(0);
+                float x[4], y[4], d[4] = {0, 0, 0, 0}, q[4] = {0, 0, 0, 0};
+                if constexpr (SLAB_IN) {
+                    unpack4(in1[ni][g], d);
+                    if constexpr (TWO_IN) unpack4(in2[ni][g], q);
+                } else if constexpr (ONE_IN) {
+                    if (in) load4<OUT>(o.aux_in + at, d);
+                    if constexpr (TWO_IN) {
+                        if (in) load4<OUT>(o.aux_in2 + at, q);
+                    }
+                }
+                epilogue4<EPI>(v, u, x, y, d, q);
+                constexpr bool X = kHasX<EPI>, Y = kHasY<EPI>;
+                if constexpr (STAGE) {
+                    put(0, 4 * ni + g, v);
+                    if constexpr (X) put(1, 4 * ni + g, x);
+                    if constexpr (Y) put(2, 4 * ni + g, y);
+                } else if (in) {
+                    store4<OUT>(o.out + at, v);
+                    if constexpr (X) store4<OUT>((EPI == kEpiSiluMulBwd ? o.out2 : o.aux_out) + at, x);
+                    if constexpr (Y) store4<OUT>(o.aux_out2 + at, y);
+                }
             }
+            __builtin_amdgcn_sched_barrier(0);
         }
         if constexpr (STAGE) {
             asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
@@ -598,24 +636,25 @@ __device__ __forceinline__ void ragged_tile(char* smem, const Operand (*op)[3], 
 // both operands' panels.
 constexpr int kGroupedRows = 8;
 
-// H: rows of a tile.  256: one workgroup a compute unit, a group's last rows
-// (at most 128) as a tile of half the height.  128: two workgroups a compute
-// unit, one's loads and stores beside the other's products.
-template <int H>
+// H x W: rows and columns of a tile (DUAL: W = 256, of which each product has
+// 128).  256 rows: one workgroup a compute unit, a group's last rows (at most
+// 128) as a tile of half the height.  128: two workgroups a compute unit, one's
+// loads and stores beside the other's products.
+template <int H, int W>
 struct TileShape {
-    static constexpr int kHalfStages = H == 256 ? 5 : 3;
-    static constexpr int kLds = H == 256 ? kStages * kStageBytes : 3 * 3 * kPanelBytes;
+    static constexpr int kHalfStages = H == 256 ? 5 : W == 256 ? 3 : 4;
+    static constexpr int kLds = H == 256 ? kStages * kStageBytes : kHalfStages * (1 + W / 128) * kPanelBytes;
     static constexpr int kPerCu = H == 256 ? 1 : 2;
 };
 
-template <int DT, bool BK, int EPI, int OUT, int H, bool SPLIT>
-__global__ __launch_bounds__(kGemmThreads, TileShape<H>::kPerCu) void grouped_gemm_kernel(GroupedParams P) {
+template <int DT, bool BK, int EPI, int OUT, int H, int W, bool SPLIT>
+__global__ __launch_bounds__(kGemmThreads, (TileShape<H, W>::kPerCu)) void grouped_gemm_kernel(GroupedParams P) {
     constexpr int ES = GElt<DT>::kBytes, KT = GElt<DT>::kKt;
     constexpr bool DUAL = EPI == kEpiSiluMul || EPI == kEpiSiluMulSave;
     constexpr int OES = OUT == kBf16 ? 2 : 4;
-    __shared__ __attribute__((aligned(1024))) char smem[TileShape<H>::kLds];
-    constexpr int W = DUAL ? 128 : 256;
-    const int tn = (P.N + W - 1) / W;
+    __shared__ __attribute__((aligned(1024))) char smem[TileShape<H, W>::kLds];
+    constexpr int TW = DUAL ? 128 : W;  // columns of the output
+    const int tn = (P.N + TW - 1) / TW;
     Groups<H> groups{P.row_offsets, P.E, P.M};
     const int ntiles = groups.count() * tn;
     const int nseg = SPLIT ? P.nseg : 1;
@@ -628,7 +667,7 @@ __global__ __launch_bounds__(kGemmThreads, TileShape<H>::kPerCu) void grouped_ge
     grouped_tile(g.local, (g.rows + H - 1) / H, tn, kGroupedRows, tm, tq);
     const int mr = min(H, g.rows - H * tm);
     const int64_t row = (int64_t)g.row0 + H * tm;
-    const int n0 = tq * W;
+    const int n0 = tq * TW;
     int k0 = 0, K = P.K;
     if constexpr (SPLIT) {  // the segment's K
         const int nk = (P.K + KT - 1) / KT;
@@ -669,12 +708,12 @@ __global__ __launch_bounds__(kGemmThreads, TileShape<H>::kPerCu) void grouped_ge
     const int sets = EPI == kEpiNone && P.a2 ? 2 : 1;
     if constexpr (H == 256) {
         if (mr > 128) {
-            ragged_tile<DT, true, BK, EPI, OUT, false, kStages, SPLIT>(smem, op, lda_b, ldb_b, K, sets, o);
+            ragged_tile<DT, true, BK, EPI, OUT, 2, W / 128, kStages, SPLIT>(smem, op, lda_b, ldb_b, K, sets, o);
             return;
         }
     }
-    ragged_tile<DT, true, BK, EPI, OUT, true, TileShape<H>::kHalfStages, SPLIT>(smem, op, lda_b, ldb_b,
-                                                                                K, sets, o);
+    ragged_tile<DT, true, BK, EPI, OUT, 1, W / 128, TileShape<H, W>::kHalfStages, SPLIT>(
+        smem, op, lda_b, ldb_b, K, sets, o);
 }
 
 // The second launch of a split product: a workgroup a row and 1024 columns,
@@ -731,12 +770,12 @@ __global__ __launch_bounds__(kGemmThreads) void grouped_join_kernel(GroupedParam
 // Weight gradients: C_e [K x N], the reduction along the group's rows; both
 // operands are read as they lie, row by row.  Groups in order, a group's
 // tiles four high; groups without rows store zeros.
-template <int DT, int OUT, int H>
-__global__ __launch_bounds__(kGemmThreads, TileShape<H>::kPerCu) void grouped_wgrad_kernel(GroupedParams P) {
+template <int DT, int OUT, int H, int W>
+__global__ __launch_bounds__(kGemmThreads, (TileShape<H, W>::kPerCu)) void grouped_wgrad_kernel(GroupedParams P) {
     constexpr int ES = GElt<DT>::kBytes, KT = GElt<DT>::kKt;
     constexpr int OES = OUT == kBf16 ? 2 : 4;
-    __shared__ __attribute__((aligned(1024))) char smem[TileShape<H>::kLds];
-    const int tk = (P.K + H - 1) / H, tn = (P.N + 255) / 256;
+    __shared__ __attribute__((aligned(1024))) char smem[TileShape<H, W>::kLds];
+    const int tk = (P.K + H - 1) / H, tn = (P.N + W - 1) / W;
     const int per = tk * tn, ntiles = P.E * per;
     const int t = xcd_chunked(blockIdx.x, ntiles, kDstdChunk);
     const int e = t / per;
@@ -750,22 +789,22 @@ __global__ __launch_bounds__(kGemmThreads, TileShape<H>::kPerCu) void grouped_wg
     const char* A = (const char*)P.a + (int64_t)row0 * lda_b;
     const char* D = (const char*)P.b + (int64_t)row0 * ldb_b;
     const Operand oa = operand_n(A, lda_b, (int64_t)tm * H * ES, (int64_t)P.K * ES, rows);
-    const Operand ob = operand_n(D, ldb_b, (int64_t)tq * 256 * ES, (int64_t)P.N * ES, rows);
+    const Operand ob = operand_n(D, ldb_b, (int64_t)tq * W * ES, (int64_t)P.N * ES, rows);
     const Operand op[2][3] = {{oa, ob, ob}, {oa, ob, ob}};
     TileOut o{};
     o.ldc = P.ldc;
     o.mr = min(H, P.K - H * tm);
-    o.n0 = tq * 256;
+    o.n0 = tq * W;
     o.N = P.N;
     o.out = (char*)P.c + ((int64_t)e * P.stride_b + (int64_t)tm * H * P.ldc) * OES;
     if constexpr (H == 256) {
         if (o.mr > 128) {
-            ragged_tile<DT, false, false, kEpiNone, OUT, false, kStages, false>(smem, op, lda_b, ldb_b, rows,
-                                                                                 1, o);
+            ragged_tile<DT, false, false, kEpiNone, OUT, 2, W / 128, kStages, false>(smem, op, lda_b, ldb_b,
+                                                                                     rows, 1, o);
             return;
         }
     }
-    ragged_tile<DT, false, false, kEpiNone, OUT, true, TileShape<H>::kHalfStages, false>(
+    ragged_tile<DT, false, false, kEpiNone, OUT, 1, W / 128, TileShape<H, W>::kHalfStages, false>(
         smem, op, lda_b, ldb_b, rows, 1, o);
 }
 
@@ -776,30 +815,33 @@ inline int64_t grouped_tiles_max(int64_t M, int E, int H, int64_t per) {
     return ((M + (int64_t)(H - 1) * ne) / H) * per;
 }
 
-template <int DT, bool BK, int EPI, int OUT, int H, bool SPLIT>
-static hipError_t grouped_go_h(const GroupedParams& p, hipStream_t s) {
-    constexpr int W = EPI == kEpiSiluMul || EPI == kEpiSiluMulSave ? 128 : 256;
-    const int64_t grid = grouped_tiles_max(p.M, p.E, H, (p.N + W - 1) / W) * (SPLIT ? p.nseg : 1);
-    hipLaunchKernelGGL((grouped_gemm_kernel<DT, BK, EPI, OUT, H, SPLIT>), dim3((unsigned)grid),
+template <int DT, bool BK, int EPI, int OUT, int H, int W, bool SPLIT>
+static hipError_t grouped_go_tile(const GroupedParams& p, hipStream_t s) {
+    constexpr int TW = EPI == kEpiSiluMul || EPI == kEpiSiluMulSave ? 128 : W;
+    const int64_t grid = grouped_tiles_max(p.M, p.E, H, (p.N + TW - 1) / TW) * (SPLIT ? p.nseg : 1);
+    hipLaunchKernelGGL((grouped_gemm_kernel<DT, BK, EPI, OUT, H, W, SPLIT>), dim3((unsigned)grid),
                        dim3(kGemmThreads), 0, s, p);
     return hipGetLastError();
 }
 
 template <int DT, bool BK, int EPI, int OUT>
 static hipError_t grouped_go(const GroupedParams& p, hipStream_t s) {
+    constexpr bool DUAL = EPI == kEpiSiluMul || EPI == kEpiSiluMulSave;
     if (p.nseg > 1) {  // few rows: the segments' kernel knows no epilogue, the join does
-        constexpr bool DUAL = EPI == kEpiSiluMul || EPI == kEpiSiluMulSave;
         constexpr int E = DUAL ? kEpiSiluMul : kEpiNone;
-        const hipError_t e = p.tile_rows == 128 ? grouped_go_h<DT, BK, E, kF32, 128, true>(p, s)
-                                                : grouped_go_h<DT, BK, E, kF32, 256, true>(p, s);
+        const hipError_t e = p.tile_rows == 128 ? grouped_go_tile<DT, BK, E, kF32, 128, 256, true>(p, s)
+                                                : grouped_go_tile<DT, BK, E, kF32, 256, 256, true>(p, s);
         if (e != hipSuccess) return e;
         hipLaunchKernelGGL((grouped_join_kernel<DT, EPI, OUT>),
                            dim3((unsigned)p.M, (unsigned)((p.N + 4 * kGemmThreads - 1) / (4 * kGemmThreads))),
                            dim3(kGemmThreads), 0, s, p);
         return hipGetLastError();
     }
-    return p.tile_rows == 128 ? grouped_go_h<DT, BK, EPI, OUT, 128, false>(p, s)
-                              : grouped_go_h<DT, BK, EPI, OUT, 256, false>(p, s);
+    if constexpr (!DUAL) {
+        if (p.tile_cols == 128) return grouped_go_tile<DT, BK, EPI, OUT, 128, 128, false>(p, s);
+    }
+    return p.tile_rows == 128 ? grouped_go_tile<DT, BK, EPI, OUT, 128, 256, false>(p, s)
+                              : grouped_go_tile<DT, BK, EPI, OUT, 256, 256, false>(p, s);
 }
 
 }  // namespace bsg

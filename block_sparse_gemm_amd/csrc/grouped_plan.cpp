@@ -24,9 +24,19 @@ static int64_t tiles_expected(int64_t M, int E, int N, int epi, int rows) {
 // experts of 256 rows, K 512, 67 / 85 us; skewed 131072 rows, K 1024, 1243 /
 // 1344 us and K 4096, 1282 / 1113 us; 8 experts of 128 rows, K 4096, 499 / 441
 // us; e4m3 8 experts of 2048 rows, K 4096, 2070 / 1852 us.
-int grouped_tile_rows(int64_t M, int E, int K, int N, int epi, int dtype, int ncu) {
+static int tile_rows(int64_t M, int E, int K, int N, int epi, int dtype, int ncu) {
     if ((int64_t)K * elt(dtype) <= 2048 || M / E <= 96) return 128;
     return M / E > 256 && tiles_expected(M, E, N, epi, 256) < ncu ? 128 : 256;
+}
+
+// Weight gradients: the reduction is a group's rows.  Short ones run two
+// workgroups a compute unit; narrower tiles where wide ones are few.
+// Measured, 128 / 256 rows a tile: 64 experts of 256 rows 53 / 62 us, of 2048
+// rows 1099 / 1071 us.
+GroupedPlan grouped_wgrad_plan(int64_t M, int K, int N, int E, int dtype, int ncu) {
+    const int64_t tn = (N + 255) / 256, few = dtype == kF32 ? 2 * (int64_t)ncu : ncu;
+    if (N <= 128 || E * (((int64_t)K + 127) / 128) * tn < few) return {128, 128, 1};
+    return {M / E <= 512 || E * (((int64_t)K + 255) / 256) * tn < few ? 128 : 256, 256, 1};
 }
 
 // K segments: a launch that would leave more than a third of the compute
@@ -38,20 +48,36 @@ int grouped_tile_rows(int64_t M, int E, int K, int N, int epi, int dtype, int nc
 // one row of two experts 41 / 178 us; e4m3, 12 rows, 93 / 138 us; but K 4096,
 // N 14336 (SILU_MUL), one row of two experts, in two segments 98 / 85 us: 224
 // workgroups fill the memory's queues already.
-int grouped_segments(int64_t M, int K, int N, int E, int epi, int dtype, int ncu) {
+//
+// Columns: 128 (under 128 rows, unsplit, one product) where the wider tile
+// would be more than half empty or leave compute units idle: fewer tiles than
+// units, of 256 rows fewer than half as many, of fp32, whose products take
+// sixteen times as long, fewer than two a unit.  Measured, 128 x 128 / wider:
+// fp32 24 experts of 96 rows, K 672, N 728, 45 / 157 us; bf16 64 experts of 256
+// rows, K 2048, N 512 (128 tiles of 256 x 256), 50 / 47 us.
+GroupedPlan grouped_plan(int64_t M, int K, int N, int E, int epi, int dtype, int ncu,
+                         int64_t max_segments) {
     constexpr int kMinSegment = 16;
     const int mats = epi == kEpiSiluMul ? 2 : 1;
     const int64_t ne = E < M ? E : M;
-    const int64_t tiles =
-        tiles_expected(M, E, N, epi, grouped_tile_rows(M, E, K, N, epi, dtype, ncu));
+    GroupedPlan p{tile_rows(M, E, K, N, epi, dtype, ncu), 256, 1};
+    const int64_t tiles = tiles_expected(M, E, N, epi, p.rows);
     const int64_t operands = (M * (int64_t)K + ne * (int64_t)K * N * mats) * elt(dtype);
     const int64_t share = M * (int64_t)N * mats * 8;
     int64_t n = 2 * (int64_t)ncu / tiles;
-    if (n < 3) return 1;
-    n = std::min(n, ((int64_t)K * elt(dtype) / 64) / kMinSegment);
-    n = std::min(n, operands / (4 * share));
-    n = std::min<int64_t>(n, kMaxSegments);
-    return n < 2 ? 1 : (int)n;
+    if (n >= 3) {
+        n = std::min(n, ((int64_t)K * elt(dtype) / 64) / kMinSegment);
+        n = std::min({n, operands / (4 * share), max_segments, (int64_t)kMaxSegments});
+        if (n >= 2) {
+            p.segments = (int)n;
+            return p;
+        }
+    }
+    if (epi != kEpiSiluMul) {
+        const int64_t few = dtype == kF32 ? 2 * (int64_t)ncu : p.rows == 256 ? ncu / 2 : ncu;
+        if (N <= 128 || (M / E > 64 && tiles < few)) p.rows = p.cols = 128;
+    }
+    return p;
 }
 
 }  // namespace bsg

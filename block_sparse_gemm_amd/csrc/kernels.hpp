@@ -169,6 +169,7 @@ struct GroupedParams {
     float* ws;             // sums of K segments (nseg > 1): [nseg][M][N], with b2 [nseg][2][M][N]
     int nseg;              // K segments
     int tile_rows;         // 128 or 256
+    int tile_cols;         // 256, or 128 (with 128 rows, unsplit)
     int64_t lda, ldb, ldc;
     int64_t stride_b;      // from an expert's matrix to the next one's  [of c]
     int64_t M;
@@ -177,8 +178,14 @@ struct GroupedParams {
 
 constexpr int kMaxSegments = 16;
 
-int grouped_tile_rows(int64_t M, int E, int K, int N, int epi, int dtype, int ncu);
-int grouped_segments(int64_t M, int K, int N, int E, int epi, int dtype, int ncu);
+// Tile rows x columns and K segments (at most max_segments) of the product (epi
+// as BSG_EPI_*) and of the weight gradient, for ncu compute units.
+struct GroupedPlan {
+    int rows, cols, segments;
+};
+GroupedPlan grouped_plan(int64_t M, int K, int N, int E, int epi, int dtype, int ncu,
+                         int64_t max_segments);
+GroupedPlan grouped_wgrad_plan(int64_t M, int K, int N, int E, int dtype, int ncu);
 
 hipError_t launch_grouped_gemm(const GroupedParams& p, int trans_b, int epi, int c_dtype, int dtype,
                                hipStream_t stream);

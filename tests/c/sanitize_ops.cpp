@@ -93,10 +93,15 @@ int main() {
                     for (int epi = BSG_EPI_NONE; epi <= BSG_EPI_SILU_MUL_BWD; ++epi) {
                         const size_t ws = bsg_grouped_gemm_workspace_bytes(M, K, N, E, epi);
                         for (int dt : {BSG_F32, BSG_BF16, BSG_E4M3}) {
-                            const int seg = bsg::grouped_segments(M, K, N, E, epi, dt, 256);
+                            const bsg::GroupedPlan p =
+                                bsg::grouped_plan(M, K, N, E, epi, dt, 256, bsg::kMaxSegments);
+                            const int seg = p.segments;
                             EXPECT(seg >= 1 && seg <= bsg::kMaxSegments);
-                            const int rows = bsg::grouped_tile_rows(M, E, K, N, epi, dt, 256);
-                            EXPECT(rows == 128 || rows == 256);
+                            EXPECT(p.rows == 128 || p.rows == 256);
+                            EXPECT(p.cols == 256 || (p.cols == 128 && p.rows == 128 && seg == 1));
+                            EXPECT(bsg::grouped_plan(M, K, N, E, epi, dt, 256, 1).segments == 1);
+                            const bsg::GroupedPlan w = bsg::grouped_wgrad_plan(M, K, N, E, dt, 256);
+                            EXPECT((w.rows == 128 || w.rows == 256) && (w.cols == 256 || w.rows == 128));
                             // the size query allows every plan
                             if (seg > 1) EXPECT(ws / ((size_t)M * N * 4) >= (size_t)seg);
                         }
