@@ -24,7 +24,7 @@ namespace {
 
 constexpr int kClipThreads = 256;
 constexpr int kList = 96;             // tensors a launch
-constexpr int kUnroll = 8;            // 16-byte vectors a thread and chunk
+constexpr int kUnroll = 4;            // 16-byte vectors a thread and chunk
 constexpr int kChunkVecs = kClipThreads * kUnroll;
 
 struct List {
@@ -262,7 +262,7 @@ hipError_t launch_grad_clip(const void* const* grads, void* const* out, const in
         List l;
         const int64_t chunks = fill(l, grads, out, counts, dtypes, n, at);
         if (l.n == 0) break;
-        const int grid = (int)std::min<int64_t>(chunks, kClipBlocks);
+        const int grid = (int)std::min<int64_t>(chunks, 65536);
         hipLaunchKernelGGL(grad_clip_kernel, dim3((unsigned)grid), dim3(kClipThreads), 0, stream, l,
                            chunks, norm, max_norm);
         const hipError_t e = hipGetLastError();

@@ -137,20 +137,26 @@ __global__ __launch_bounds__(WG) void rms_norm_kernel(NormParams p) {
         w[i] = c < vecs ? ((const u32x4*)p.weight)[c] : u32x4{0, 0, 0, 0};
     }
     const float inv_d = 1.0f / (float)p.d;
-    for (int64_t base = (int64_t)blockIdx.x * ROWS; base < p.T; base += (int64_t)gridDim.x * ROWS) {
+    auto load = [&](u32x4* v, u32x4* r, int64_t base) {
         const int64_t t = base + threadIdx.x / TPR;
-        const bool here = t < p.T;
-        u32x4 v[NV], r[NV];
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = tr + i * TPR;
-            const bool on = here && c < vecs;
+            const bool on = t < p.T && c < vecs;
             v[i] = on ? *(const u32x4*)((const char*)p.x + t * p.ldx * esz + (int64_t)c * 16)
                       : u32x4{0, 0, 0, 0};
             if (p.residual)
                 r[i] = on ? *(const u32x4*)((const char*)p.residual + t * p.ldr * esz + (int64_t)c * 16)
                           : u32x4{0, 0, 0, 0};
         }
+    };
+    const int64_t stride = (int64_t)gridDim.x * ROWS;
+    u32x4 v[NV], r[NV], vn[NV], rn[NV];
+    load(v, r, (int64_t)blockIdx.x * ROWS);
+    for (int64_t base = (int64_t)blockIdx.x * ROWS; base < p.T; base += stride) {
+        load(vn, rn, base + stride);  // the next rows' loads, in flight beside this row's work
+        const int64_t t = base + threadIdx.x / TPR;
+        const bool here = t < p.T;
         if (p.residual) {
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
@@ -223,15 +229,18 @@ __global__ __launch_bounds__(WG) void rms_norm_kernel(NormParams p) {
                 }
             }
         }
+#pragma unroll
+        for (int i = 0; i < NV; ++i) v[i] = vn[i], r[i] = rn[i];
     }
 }
 
-// The gradient: 1024 threads a workgroup, 1024 / TPR rows in hand.  Each
-// thread sums its columns' dw over all its rows; at the end the workgroup's
-// rows join in LDS in a fixed order and the partial row goes to the
-// workspace, which a second launch sums over the workgroups: no atomics, so
-// the sums are the same on every run.
-constexpr int kBwdThreads = 1024;
+// The gradient: 512 threads a workgroup, 512 / TPR rows in hand, the next
+// rows' loads in flight while these are worked on.  Each thread sums its
+// columns' dw over all its rows; at the end the workgroup's rows join in LDS in
+// a fixed order and the partial row goes to the workspace, which a second
+// launch sums over the workgroups: no atomics, so the sums are the same on
+// every run.
+constexpr int kBwdThreads = 512;
 
 template <int DT, int TPR, int NV>
 __global__ __launch_bounds__(kBwdThreads) void rms_norm_backward_kernel(NormParams p) {
@@ -252,33 +261,44 @@ __global__ __launch_bounds__(kBwdThreads) void rms_norm_backward_kernel(NormPara
         for (int j = 0; j < VN; ++j) dw[i][j] = 0.0f;
     }
     const float inv_d = 1.0f / (float)p.d;
-    for (int64_t base = (int64_t)blockIdx.x * ROWS; base < p.T; base += (int64_t)gridDim.x * ROWS) {
+    struct Row {
+        u32x4 g[NV], h[NV], e[NV];
+        float rstd;
+    };
+    auto load = [&](Row& r, int64_t base) {
         const int64_t t = base + slot;
         const bool here = t < p.T;
-        u32x4 g[NV], h[NV], e[NV];
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = tr + i * TPR;
             const bool on = here && c < vecs;
             const u32x4 zero{0, 0, 0, 0};
-            g[i] = on ? *(const u32x4*)((const char*)p.dy + t * p.ldy * esz + (int64_t)c * 16) : zero;
-            h[i] = on ? *(const u32x4*)((const char*)p.x + t * p.ldx * esz + (int64_t)c * 16) : zero;
-            e[i] = zero;
+            r.g[i] = on ? *(const u32x4*)((const char*)p.dy + t * p.ldy * esz + (int64_t)c * 16) : zero;
+            r.h[i] = on ? *(const u32x4*)((const char*)p.x + t * p.ldx * esz + (int64_t)c * 16) : zero;
+            r.e[i] = zero;
             if (p.residual)
-                e[i] = on ? *(const u32x4*)((const char*)p.residual + t * p.ldr * esz + (int64_t)c * 16)
-                          : zero;
+                r.e[i] = on ? *(const u32x4*)((const char*)p.residual + t * p.ldr * esz + (int64_t)c * 16)
+                            : zero;
         }
-        const float rstd = here ? p.rstd[t] : 0.0f;
+        r.rstd = here ? p.rstd[t] : 0.0f;
+    };
+    const int64_t stride = (int64_t)gridDim.x * ROWS;
+    Row cur, nxt;
+    load(cur, (int64_t)blockIdx.x * ROWS);
+    for (int64_t base = (int64_t)blockIdx.x * ROWS; base < p.T; base += stride) {
+        load(nxt, base + stride);  // (no row there: nothing is read)
+        const int64_t t = base + slot;
+        const bool here = t < p.T;
         float dot = 0.0f;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             float a[VN], b[VN], k[VN];
-            Vec<DT>::to_f32(g[i], a);
-            Vec<DT>::to_f32(h[i], b);
+            Vec<DT>::to_f32(cur.g[i], a);
+            Vec<DT>::to_f32(cur.h[i], b);
             Vec<DT>::to_f32(w[i], k);
 #pragma unroll
             for (int j = 0; j < VN; ++j) {
-                const float n = b[j] * rstd;
+                const float n = b[j] * cur.rstd;
                 dot = fmaf(a[j] * k[j], n, dot);
                 dw[i][j] = fmaf(a[j], n, dw[i][j]);
             }
@@ -288,16 +308,17 @@ __global__ __launch_bounds__(kBwdThreads) void rms_norm_backward_kernel(NormPara
         for (int i = 0; i < NV; ++i) {
             const int c = tr + i * TPR;
             float a[VN], b[VN], k[VN], x[VN];
-            Vec<DT>::to_f32(g[i], a);
-            Vec<DT>::to_f32(h[i], b);
+            Vec<DT>::to_f32(cur.g[i], a);
+            Vec<DT>::to_f32(cur.h[i], b);
             Vec<DT>::to_f32(w[i], k);
-            Vec<DT>::to_f32(e[i], x);
+            Vec<DT>::to_f32(cur.e[i], x);
 #pragma unroll
             for (int j = 0; j < VN; ++j)
-                x[j] = fmaf(rstd, fmaf(-(b[j] * rstd), c1, a[j] * k[j]), x[j]);
+                x[j] = fmaf(cur.rstd, fmaf(-(b[j] * cur.rstd), c1, a[j] * k[j]), x[j]);
             if (here && c < vecs)
                 *(u32x4*)((char*)p.y + t * p.ldh * esz + (int64_t)c * 16) = Vec<DT>::of_f32(x);
         }
+        cur = nxt;
     }
     // the workgroup's rows, slot by slot
     for (int s = 0; s < ROWS; ++s) {
@@ -319,25 +340,25 @@ __global__ __launch_bounds__(kBwdThreads) void rms_norm_backward_kernel(NormPara
     }
 }
 
-// dw[c] = the sum of the workgroups' partial rows: 64 columns a workgroup,
-// its 16 waves every sixteenth row, joined in LDS in wave order.
+// dw[c] = the sum of the workgroups' partial rows: 16 columns a workgroup, its
+// 64 groups of 16 lanes every 64th row, joined in LDS in group order.
 __global__ __launch_bounds__(1024) void rms_norm_dw_kernel(const float* __restrict__ partial,
                                                            int rows, int d,
                                                            float* __restrict__ dw) {
-    __shared__ float part[16][kWave];
-    const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
-    const int c = blockIdx.x * kWave + lane;
+    __shared__ float part[64][17];
+    const int lane = threadIdx.x % 16, group = threadIdx.x / 16;
+    const int c = blockIdx.x * 16 + lane;
     float s = 0.0f;
     if (c < d) {
 #pragma unroll 8
-        for (int r = wave; r < rows; r += 16) s += partial[(int64_t)r * d + c];
+        for (int r = group; r < rows; r += 64) s += partial[(int64_t)r * d + c];
     }
-    part[wave][lane] = s;
+    part[group][lane] = s;
     __syncthreads();
-    if (wave == 0 && c < d) {
+    if (group == 0 && c < d) {
         s = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) s += part[i][lane];
+        for (int i = 0; i < 64; ++i) s += part[i][lane];
         dw[c] = s;
     }
 }
@@ -376,15 +397,15 @@ hipError_t bwd_pick(const NormParams& p, int grid, hipStream_t s) {
     if (vecs <= 64) return bwd_go<DT, 64, 1>(p, grid, s);
     if (vecs <= 128) return bwd_go<DT, 64, 2>(p, grid, s);
     if (vecs <= 256) return bwd_go<DT, 256, 1>(p, grid, s);
-    if (vecs <= 512) return bwd_go<DT, 512, 1>(p, grid, s);
-    if (vecs <= 1024) return bwd_go<DT, 1024, 1>(p, grid, s);
-    return bwd_go<DT, 1024, 2>(p, grid, s);
+    if (vecs <= 512) return bwd_go<DT, 256, 2>(p, grid, s);
+    if (vecs <= 1024) return bwd_go<DT, 512, 2>(p, grid, s);
+    return bwd_go<DT, 512, 4>(p, grid, s);
 }
 
 // Threads that share a row in the backward, as bwd_pick chooses them.
 int bwd_tpr(int dtype, int d) {
     const int vecs = d / (dtype == kBf16 ? 8 : 4);
-    return vecs <= 128 ? 64 : vecs <= 256 ? 256 : vecs <= 512 ? 512 : 1024;
+    return vecs <= 128 ? 64 : vecs <= 512 ? 256 : 512;
 }
 
 }  // namespace
@@ -405,7 +426,7 @@ hipError_t launch_rms_norm_backward(const NormParams& p, int dtype, float* dweig
         const hipError_t e = dtype == kBf16 ? bwd_pick<kBf16>(p, grid, s) : bwd_pick<kF32>(p, grid, s);
         if (e != hipSuccess) return e;
     }
-    hipLaunchKernelGGL(rms_norm_dw_kernel, dim3((unsigned)((p.d + kWave - 1) / kWave)), dim3(1024), 0,
+    hipLaunchKernelGGL(rms_norm_dw_kernel, dim3((unsigned)((p.d + 15) / 16)), dim3(1024), 0,
                        s, p.partial, grid, p.d, dweight);
     return hipGetLastError();
 }
