@@ -383,7 +383,7 @@ def _rows(call, name, t, shape, dtype):
     ld, one = t.stride()
     if one != 1 and shape[1] > 1 and shape[0]:
         _fail(call, f"{name} must be row-major")
-    return ld if shape[0] > 1 or ld > shape[1] else shape[1]
+    return ld if shape[0] > 1 else shape[1]   # one row has no stride to speak of
 
 
 def _vector(call, name, t, n, dtype):
@@ -461,7 +461,7 @@ def _matrices(call, name, t, shape, dtype):
     stride, ld, one = t.stride()
     if one != 1 and shape[2] > 1:
         _fail(call, f"{name} must have contiguous rows")
-    return ld if shape[1] > 1 or ld > shape[2] else shape[2], stride
+    return ld if shape[1] > 1 else shape[2], stride if shape[0] > 1 else 16
 
 
 def _code_of(epilogue):

@@ -149,6 +149,9 @@ static int grouped_elt_bytes(int dtype) { return dtype == BSG_E4M3 ? 1 : elt_byt
 // query has no stream to ask).
 constexpr int kPlanCus = 256;
 
+// Workgroups of 256 threads that one launch may have (2^32 threads).
+constexpr int64_t kMaxGrid = (int64_t(1) << 24) - 1;
+
 size_t bsg_grouped_gemm_workspace_bytes(int64_t M, int K, int N, int E, int epilogue) {
     if (M < 0 || M > INT32_MAX || K < 1 || K > kMaxWidth || N < 1 || N > kMaxWidth || E < 1 ||
         E > BSG_MAX_EXPERTS || epilogue < BSG_EPI_NONE || epilogue > BSG_EPI_SILU_MUL_BWD)
@@ -228,10 +231,6 @@ bsg_status bsg_grouped_gemm(const void* a, const void* a2, int64_t lda, const fl
     if (M == 0) return ok();
     REQUIRE_VEC_PTR(a);
     REQUIRE_VEC_PTR(c);
-    // tiles of the smaller kind (128 x 128), in most segments
-    const int64_t ne = std::min<int64_t>(E, M);
-    if (((M + 127 * ne) / 128) * ((N + 127) / 128) * bsg::kMaxSegments > INT32_MAX)
-        return fail(BSG_EUNSUPPORTED, "too many tiles");
     bsg::GroupedParams p{};
     p.a = a;
     p.a2 = a2;
@@ -247,6 +246,9 @@ bsg_status bsg_grouped_gemm(const void* a, const void* a2, int64_t lda, const fl
     const int64_t share = M * N * (epilogue == BSG_EPI_SILU_MUL ? 2 : 1) * (int64_t)sizeof(float);
     const int64_t fit = workspace ? (int64_t)std::min<size_t>(workspace_bytes, INT64_MAX) / share : 1;
     const bsg::GroupedPlan plan = bsg::grouped_plan(M, K, N, E, epilogue, dtype, kPlanCus, fit);
+    const int64_t ne = std::min<int64_t>(E, M), w = epilogue == BSG_EPI_SILU_MUL ? 128 : plan.cols;
+    if ((M + (plan.rows - 1) * ne) / plan.rows * ((N + w - 1) / w) * plan.segments > kMaxGrid)
+        return fail(BSG_EUNSUPPORTED, "too many tiles for one launch");
     p.ws = (float*)workspace;
     p.nseg = plan.segments;
     p.tile_rows = plan.rows;
@@ -293,8 +295,9 @@ bsg_status bsg_grouped_wgrad(const void* a, int64_t lda, const void* dmat, int64
         REQUIRE_VEC_PTR(a);
         REQUIRE_VEC_PTR(dmat);
     }
-    if ((int64_t)E * ((K + 127) / 128) * ((N + 127) / 128) > INT32_MAX)
-        return fail(BSG_EUNSUPPORTED, "too many tiles");
+    const bsg::GroupedPlan plan = bsg::grouped_wgrad_plan(M, K, N, E, dtype, kPlanCus);
+    if ((int64_t)E * ((K + plan.rows - 1) / plan.rows) * ((N + plan.cols - 1) / plan.cols) > kMaxGrid)
+        return fail(BSG_EUNSUPPORTED, "too many tiles for one launch");
     bsg::GroupedParams p{};
     p.a = a;
     p.b = dmat;
@@ -308,7 +311,6 @@ bsg_status bsg_grouped_wgrad(const void* a, int64_t lda, const void* dmat, int64
     p.K = K;
     p.N = N;
     p.E = E;
-    const bsg::GroupedPlan plan = bsg::grouped_wgrad_plan(M, K, N, E, dtype, kPlanCus);
     p.tile_rows = plan.rows;
     p.tile_cols = plan.cols;
     return hip_status(bsg::launch_grouped_wgrad(p, c_dtype, dtype, (hipStream_t)stream),

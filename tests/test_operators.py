@@ -414,6 +414,73 @@ def test_grouped_gemm_two_sets(dtype, trans, K, N):
     close("c", c, p, u(dtype) * p.abs() + e_sum(2 * K, s))
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32, E4M3])
+@pytest.mark.parametrize("epi", ["none", "gelu", "silu_mul"])
+def test_grouped_gemm_split_along_k(dtype, epi):
+    """Few rows, a long sum: workspaces that hold every number of segments,
+    the same bits on every run, nothing behind the workspace's end touched."""
+    sizes, K, N = [1, 0, 5, 2], 4112, 136
+    E, M = len(sizes), sum(sizes)
+    g = gen(8)
+    trans, cdt = dtype == E4M3, BF16 if dtype == E4M3 else dtype
+    off = offsets(sizes)
+    a = torch.randn(M, K, generator=g, device="cuda").to(dtype)
+    two = epi == "silu_mul"
+    b = [weights(g, E, K, N, dtype, trans, "apart") for _ in range(2 if two else 1)]
+    sa = sb = None
+    scale = 1.0 / math.sqrt(K)
+    if dtype == E4M3:
+        sa = torch.ones(M, device="cuda")
+        sb = torch.full((len(b), E, N), scale, device="cuda")
+    else:
+        for w in b:
+            w.mul_(scale)
+            scale = 1.0
+    share = M * N * len(b)
+    most = bsg.grouped_gemm_workspace_bytes(M, K, N, E, epi) // 4
+    assert most >= 4 * share
+    ps = [products_exact(a.float(), w.float(), off, trans) for w in b]
+    f = 1.0 / math.sqrt(K) if dtype == E4M3 else 1.0
+    ps = [(p * f, s * f) for p, s in ps]
+    if epi == "none":
+        want, slope = ps[0][0], [torch.ones_like(ps[0][0])]
+    else:
+        out, k = acts_exact(epi, ps[0][0], ps[1][0] if two else None, None)
+        want, slope = out[0], list(k[0])
+    for floats in (0, share, 2 * share, 3 * share + 1, most):
+        ws = torch.full((floats + 64,), 7.0, device="cuda")
+        got = []
+        for _ in range(2):
+            c = torch.full((M, N), 9.0, device="cuda", dtype=cdt)
+            bsg.grouped_gemm(a, off, b[0], c, epilogue=epi, trans_b=trans, b2=b[1] if two else None,
+                             a_scale=sa, b_scale=sb, workspace=ws[:floats] if floats else None)
+            got.append(c)
+        assert torch.equal(got[0], got[1]) and bool((ws[floats:] == 7).all())
+        err = slope[0] * e_sum(K, ps[0][1], dtype)
+        if two:
+            err = err + slope[1] * e_sum(K, ps[1][1], dtype)
+        own = 8 * STEP * (want.abs() + ps[0][0].abs() * (1 + (ps[1][0].abs() if two else 0)) + 1)
+        close(f"{floats} floats", got[0], want, u(cdt) * want.abs() + err + own)
+
+
+def test_grouped_gemm_single_row_and_expert_strides():
+    """One row, and one expert: strides that no address depends on may be odd."""
+    g = gen(2)
+    a, b = randn(g, 1, 64, dtype=BF16), randn(g, 1, 64, 72, dtype=BF16)
+    off = offsets([1])
+    want = torch.empty(1, 72, device="cuda", dtype=BF16)
+    bsg.grouped_gemm(a, off, b, want)
+    odd = torch.as_strided(a, (1, 64), (67, 1))
+    oddb = torch.as_strided(b, (1, 64, 72), (4611, 72, 1))
+    got = torch.empty_like(want)
+    bsg.grouped_gemm(odd, off, oddb, torch.as_strided(got, (1, 72), (75, 1)))
+    assert torch.equal(got, want)
+    y, y2, w = torch.empty_like(a), torch.empty_like(a), a[0].clone()
+    bsg.rms_norm(a, w, EPS, y)
+    bsg.rms_norm(odd, w, EPS, torch.as_strided(y2, (1, 64), (71, 1)))
+    assert torch.equal(y, y2)
+
+
 def test_grouped_gemm_groups_do_not_mix():
     """NaN and infinity in one expert's rows and weights stay with that expert."""
     sizes = [40, 70, 300, 10]

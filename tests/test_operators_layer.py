@@ -149,9 +149,11 @@ def test_ragged_layer_forward_and_backward(shape):
         assert d <= tol * b.abs().max().item(), (name, d, b.abs().max().item())
 
 
-def test_ragged_layer_agrees_with_the_padded_one():
+@pytest.mark.parametrize("yp", ["bf16", "f32"])
+def test_ragged_layer_agrees_with_the_padded_one(yp):
     shape = (700, 128, 6, 256, 2, "swiglu", "bf16", True)
     s, t = make_layer(*shape)
+    s.yp_dtype = yp
     outs = []
     for rows in (1, 128):
         s.bin_rows = rows
