@@ -44,10 +44,12 @@ GroupedPlan grouped_wgrad_plan(int64_t M, int K, int N, int E, int dtype, int nc
 // each of them, if a segment keeps kMinSegment K-tiles (64 bytes of K a row
 // each) or more and the segments' sums, written and read once in fp32, stay
 // below a quarter of the operands' bytes.  Measured, split / not: bf16, K
-// 14336, N 4096, 8 experts of 12 rows 165 / 212 us, of 128 rows 220 / 293 us,
-// one row of two experts 41 / 178 us; e4m3, 12 rows, 93 / 138 us; but K 4096,
-// N 14336 (SILU_MUL), one row of two experts, in two segments 98 / 85 us: 224
-// workgroups fill the memory's queues already.
+// 14336, N 4096, 8 experts of 128 rows 220 / 293 us, one row of two experts 41
+// / 178 us; but K 4096, N 14336 (SILU_MUL), one row of two experts, in two
+// segments 98 / 85 us: 224 workgroups fill the memory's queues already.  Nor
+// are groups of few rows split whose narrow tiles fill the units: K 14336, N
+// 4096, 8 experts of 12 rows, four segments / 128 columns, bf16 165 / 145 us,
+// e4m3 93 / 88 us.
 //
 // Columns: 128 (under 128 rows, unsplit, one product) where the wider tile
 // would be more than half empty or leave compute units idle: fewer tiles than
@@ -58,14 +60,16 @@ GroupedPlan grouped_wgrad_plan(int64_t M, int K, int N, int E, int dtype, int nc
 GroupedPlan grouped_plan(int64_t M, int K, int N, int E, int epi, int dtype, int ncu,
                          int64_t max_segments) {
     constexpr int kMinSegment = 16;
-    const int mats = epi == kEpiSiluMul ? 2 : 1;
+    const bool dual = epi == kEpiSiluMul;
+    const int mats = dual ? 2 : 1;
     const int64_t ne = E < M ? E : M;
     GroupedPlan p{tile_rows(M, E, K, N, epi, dtype, ncu), 256, 1};
     const int64_t tiles = tiles_expected(M, E, N, epi, p.rows);
-    const int64_t operands = (M * (int64_t)K + ne * (int64_t)K * N * mats) * elt(dtype);
-    const int64_t share = M * (int64_t)N * mats * 8;
+    const bool narrow_fills = M / E <= 96 && 2 * tiles >= ncu;
     int64_t n = 2 * (int64_t)ncu / tiles;
-    if (n >= 3) {
+    if (n >= 3 && (dual || !narrow_fills)) {
+        const int64_t operands = (M * (int64_t)K + ne * (int64_t)K * N * mats) * elt(dtype);
+        const int64_t share = M * (int64_t)N * mats * 8;
         n = std::min(n, ((int64_t)K * elt(dtype) / 64) / kMinSegment);
         n = std::min({n, operands / (4 * share), max_segments, (int64_t)kMaxSegments});
         if (n >= 2) {
@@ -73,9 +77,9 @@ GroupedPlan grouped_plan(int64_t M, int K, int N, int E, int epi, int dtype, int
             return p;
         }
     }
-    if (epi != kEpiSiluMul) {
+    if (!dual) {
         const int64_t few = dtype == kF32 ? 2 * (int64_t)ncu : p.rows == 256 ? ncu / 2 : ncu;
-        if (N <= 128 || (M / E > 64 && tiles < few)) p.rows = p.cols = 128;
+        if (N <= 128 || ((M / E > 64 || narrow_fills) && tiles < few)) p.rows = p.cols = 128;
     }
     return p;
 }
