@@ -36,7 +36,8 @@ SYMBOLS = ("bsg_max_padded_rows", "bsg_topology_sizes", "bsg_route_workspace_byt
            "bsg_dsd_combine_top1", "bsg_dstd",
            "bsg_unpermute_combine", "bsg_rms_norm", "bsg_rms_norm_backward",
            "bsg_rms_norm_backward_workspace_bytes", "bsg_grouped_gemm",
-           "bsg_grouped_gemm_workspace_bytes", "bsg_grouped_wgrad", "bsg_grad_norm",
+           "bsg_grouped_gemm_workspace_bytes", "bsg_grouped_wgrad",
+           "bsg_grouped_wgrad_workspace_bytes", "bsg_grad_norm",
            "bsg_grad_norm_workspace_bytes", "bsg_grad_clip", "bsg_stream_copy", "bsg_status_string", "bsg_last_error")
 
 
@@ -133,7 +134,9 @@ def lib():
                                        i32, i32, i32, vp, vp, i64, i32, vp, i32, vp, sz, vp]
         L.bsg_grouped_wgrad.restype = i32
         L.bsg_grouped_wgrad.argtypes = [vp, i64, vp, i64, vp, i32, i64, i32, i32, vp, i64, i64,
-                                        i32, i32, vp]
+                                        i32, i32, vp, sz, vp]
+        L.bsg_grouped_wgrad_workspace_bytes.restype = sz
+        L.bsg_grouped_wgrad_workspace_bytes.argtypes = [i64, i32, i32, i32]
         L.bsg_grad_norm_workspace_bytes.restype = sz
         L.bsg_grad_norm_workspace_bytes.argtypes = []
         L.bsg_grad_norm.restype = i32
@@ -526,11 +529,17 @@ def grouped_gemm(a, row_offsets, b, c, epilogue="none", trans_b=False, a2=None, 
         _address(workspace), _nbytes(call, workspace), stream))
 
 
-def grouped_wgrad(a, dmat, row_offsets, c):
+def grouped_wgrad_workspace_bytes(M: int, K: int, N: int, E: int) -> int:
+    """Bytes of a workspace that lets grouped_wgrad split long groups (0: it
+    never splits this one)."""
+    return int(lib().bsg_grouped_wgrad_workspace_bytes(M, K, N, E))
+
+
+def grouped_wgrad(a, dmat, row_offsets, c, workspace=None):
     """c[e] = a[rows of e]^T @ dmat[rows of e]: c is an [E, K, N] view with
     contiguous rows, of a's type or fp32."""
     call = "grouped_wgrad"
-    stream = _current(call, (a, dmat, row_offsets, c))
+    stream = _current(call, (a, dmat, row_offsets, c, workspace))
     if a.dim() != 2 or dmat.dim() != 2 or c.dim() != 3:
         _fail(call, "a is [M, K], dmat [M, N], c one matrix an expert")
     M, K = a.shape
@@ -541,7 +550,8 @@ def grouped_wgrad(a, dmat, row_offsets, c):
     _vector(call, "row_offsets", row_offsets, E + 1, torch.int32)
     _check(call, lib().bsg_grouped_wgrad(
         a.data_ptr(), lda, dmat.data_ptr(), ldd, row_offsets.data_ptr(), E, M, K, N, c.data_ptr(),
-        ldc, stride, dtype_code(c), dtype_code(a), stream))
+        ldc, stride, dtype_code(c), dtype_code(a), _address(workspace), _nbytes(call, workspace),
+        stream))
 
 
 def _tensor_list(call, name, tensors):

@@ -266,10 +266,20 @@ bsg_status bsg_grouped_gemm(const void* a, const void* a2, int64_t lda, const fl
                       "grouped_gemm");
 }
 
+size_t bsg_grouped_wgrad_workspace_bytes(int64_t M, int K, int N, int E) {
+    if (M < 0 || M > INT32_MAX || K < 1 || K > kMaxWidth || N < 1 || N > kMaxWidth || E < 1 ||
+        E > BSG_MAX_EXPERTS)
+        return 0;
+    int n = 1;
+    for (const int dtype : {BSG_F32, BSG_BF16})
+        n = std::max(n, bsg::grouped_wgrad_plan(M, K, N, E, dtype, kPlanCus, bsg::kMaxSegments).segments);
+    return n == 1 ? 0 : (size_t)n * E * K * N * sizeof(float);
+}
+
 bsg_status bsg_grouped_wgrad(const void* a, int64_t lda, const void* dmat, int64_t ldd,
                              const int32_t* row_offsets, int E, int64_t M, int K, int N, void* c,
                              int64_t ldc, int64_t stride_c, int c_dtype, int dtype,
-                             bsg_stream_t stream) {
+                             void* workspace, size_t workspace_bytes, bsg_stream_t stream) {
     REQUIRE(dtype_ok(dtype), "unknown dtype %d", dtype);
     REQUIRE(dtype_ok(c_dtype), "unknown c_dtype %d", c_dtype);
     if (dtype == BSG_F32 && c_dtype != BSG_F32)
@@ -295,10 +305,19 @@ bsg_status bsg_grouped_wgrad(const void* a, int64_t lda, const void* dmat, int64
         REQUIRE_VEC_PTR(a);
         REQUIRE_VEC_PTR(dmat);
     }
-    const bsg::GroupedPlan plan = bsg::grouped_wgrad_plan(M, K, N, E, dtype, kPlanCus);
-    if ((int64_t)E * ((K + plan.rows - 1) / plan.rows) * ((N + plan.cols - 1) / plan.cols) > kMaxGrid)
+    REQUIRE(workspace == nullptr || aligned(workspace, 16), "workspace must be 16-byte aligned");
+    // segments as many as planned, or as the workspace holds (a share's bytes
+    // may pass 2^63: compared as a quotient)
+    const int64_t fit = workspace ? (int64_t)std::min<size_t>(workspace_bytes, INT64_MAX) / 4 /
+                                        ((int64_t)K * N) / E
+                                  : 1;
+    const bsg::GroupedPlan plan = bsg::grouped_wgrad_plan(M, K, N, E, dtype, kPlanCus, fit);
+    if ((int64_t)E * ((K + plan.rows - 1) / plan.rows) * ((N + plan.cols - 1) / plan.cols) *
+            plan.segments > kMaxGrid)
         return fail(BSG_EUNSUPPORTED, "too many tiles for one launch");
     bsg::GroupedParams p{};
+    p.ws = (float*)workspace;
+    p.nseg = plan.segments;
     p.a = a;
     p.b = dmat;
     p.row_offsets = row_offsets;

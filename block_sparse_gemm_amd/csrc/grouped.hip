@@ -3,18 +3,27 @@
 
 namespace bsg {
 
-template <int DT, int OUT, int H, int W>
+template <int DT, int OUT, int H, int W, bool SPLIT>
 static hipError_t wgrad_tile(const GroupedParams& p, hipStream_t s) {
-    const int64_t grid = (int64_t)p.E * ((p.K + H - 1) / H) * ((p.N + W - 1) / W);
-    hipLaunchKernelGGL((grouped_wgrad_kernel<DT, OUT, H, W>), dim3((unsigned)grid), dim3(kGemmThreads),
+    const int64_t grid = (int64_t)p.E * ((p.K + H - 1) / H) * ((p.N + W - 1) / W) * (SPLIT ? p.nseg : 1);
+    hipLaunchKernelGGL((grouped_wgrad_kernel<DT, OUT, H, W, SPLIT>), dim3((unsigned)grid), dim3(kGemmThreads),
                        0, s, p);
     return hipGetLastError();
 }
 
 template <int DT, int OUT>
 static hipError_t wgrad_go(const GroupedParams& p, hipStream_t s) {
-    if (p.tile_cols == 128) return wgrad_tile<DT, OUT, 128, 128>(p, s);
-    return p.tile_rows == 128 ? wgrad_tile<DT, OUT, 128, 256>(p, s) : wgrad_tile<DT, OUT, 256, 256>(p, s);
+    if (p.nseg > 1) {
+        const hipError_t e = wgrad_tile<DT, kF32, 128, 128, true>(p, s);
+        if (e != hipSuccess) return e;
+        hipLaunchKernelGGL(grouped_wgrad_join_kernel<OUT>,
+                           dim3((unsigned)(p.E * p.K), (unsigned)((p.N + 4 * kGemmThreads - 1) / (4 * kGemmThreads))),
+                           dim3(kGemmThreads), 0, s, p);
+        return hipGetLastError();
+    }
+    if (p.tile_cols == 128) return wgrad_tile<DT, OUT, 128, 128, false>(p, s);
+    return p.tile_rows == 128 ? wgrad_tile<DT, OUT, 128, 256, false>(p, s)
+                              : wgrad_tile<DT, OUT, 256, 256, false>(p, s);
 }
 
 hipError_t launch_grouped_wgrad(const GroupedParams& p, int c_dtype, int dtype, hipStream_t s) {

@@ -770,14 +770,16 @@ __global__ __launch_bounds__(kGemmThreads) void grouped_join_kernel(GroupedParam
 // Weight gradients: C_e [K x N], the reduction along the group's rows; both
 // operands are read as they lie, row by row.  Groups in order, a group's
 // tiles four high; groups without rows store zeros.
-template <int DT, int OUT, int H, int W>
+// SPLIT: P.nseg segments of each group's rows, their sums to the workspace.
+template <int DT, int OUT, int H, int W, bool SPLIT>
 __global__ __launch_bounds__(kGemmThreads, (TileShape<H, W>::kPerCu)) void grouped_wgrad_kernel(GroupedParams P) {
     constexpr int ES = GElt<DT>::kBytes, KT = GElt<DT>::kKt;
     constexpr int OES = OUT == kBf16 ? 2 : 4;
     __shared__ __attribute__((aligned(1024))) char smem[TileShape<H, W>::kLds];
     const int tk = (P.K + H - 1) / H, tn = (P.N + W - 1) / W;
     const int per = tk * tn, ntiles = P.E * per;
-    const int t = xcd_chunked(blockIdx.x, ntiles, kDstdChunk);
+    const int seg = SPLIT ? blockIdx.x / ntiles : 0;
+    const int t = SPLIT ? (int)blockIdx.x - seg * ntiles : xcd_chunked(blockIdx.x, ntiles, kDstdChunk);
     const int e = t / per;
     int tm, tq;
     grouped_tile(t - e * per, tk, tn, 4, tm, tq);
@@ -785,6 +787,13 @@ __global__ __launch_bounds__(kGemmThreads, (TileShape<H, W>::kPerCu)) void group
     group_rows(P.row_offsets, e, P.M, row0, rows);
     row0 = __builtin_amdgcn_readfirstlane(row0);
     rows = __builtin_amdgcn_readfirstlane(rows);
+    if constexpr (SPLIT) {  // the segment's rows
+        const int nk = (rows + KT - 1) / KT;
+        const int k0 = (int)((int64_t)nk * seg / P.nseg) * KT;
+        const int k1 = min(rows, (int)((int64_t)nk * (seg + 1) / P.nseg) * KT);
+        row0 += k0;
+        rows = max(k1 - k0, 0);
+    }
     const int64_t lda_b = P.lda * ES, ldb_b = P.ldb * ES;
     const char* A = (const char*)P.a + (int64_t)row0 * lda_b;
     const char* D = (const char*)P.b + (int64_t)row0 * ldb_b;
@@ -797,15 +806,36 @@ __global__ __launch_bounds__(kGemmThreads, (TileShape<H, W>::kPerCu)) void group
     o.n0 = tq * W;
     o.N = P.N;
     o.out = (char*)P.c + ((int64_t)e * P.stride_b + (int64_t)tm * H * P.ldc) * OES;
+    if constexpr (SPLIT) o.part = P.ws + (((int64_t)seg * P.E + e) * P.K + (int64_t)tm * H) * P.N;
     if constexpr (H == 256) {
         if (o.mr > 128) {
-            ragged_tile<DT, false, false, kEpiNone, OUT, 2, W / 128, kStages, false>(smem, op, lda_b, ldb_b,
+            ragged_tile<DT, false, false, kEpiNone, OUT, 2, W / 128, kStages, SPLIT>(smem, op, lda_b, ldb_b,
                                                                                      rows, 1, o);
             return;
         }
     }
-    ragged_tile<DT, false, false, kEpiNone, OUT, 1, W / 128, TileShape<H, W>::kHalfStages, false>(
+    ragged_tile<DT, false, false, kEpiNone, OUT, 1, W / 128, TileShape<H, W>::kHalfStages, SPLIT>(
         smem, op, lda_b, ldb_b, rows, 1, o);
+}
+
+// The second launch of a split weight gradient: row k of expert e, the
+// segments' sums added in order.
+template <int OUT>
+__global__ __launch_bounds__(kGemmThreads) void grouped_wgrad_join_kernel(GroupedParams P) {
+    constexpr int OES = OUT == kBf16 ? 2 : 4;
+    const int64_t row = blockIdx.x;  // e K + k
+    const int col = (blockIdx.y * kGemmThreads + threadIdx.x) * 4;
+    if (col >= P.N) return;
+    const int64_t share = (int64_t)P.E * P.K * P.N;
+    float v[4] = {0, 0, 0, 0};
+#pragma unroll 4
+    for (int i = 0; i < P.nseg; ++i) {
+        const f32x4 p = *(const f32x4*)(P.ws + i * share + row * P.N + col);
+#pragma unroll
+        for (int s = 0; s < 4; ++s) v[s] += p[s];
+    }
+    const int64_t e = row / P.K, k = row - e * P.K;
+    store4<OUT>((char*)P.c + (e * P.stride_b + k * P.ldc + col) * OES, v);
 }
 
 // Most tiles of M rows in E groups, `per` tiles a row tile of H rows: every

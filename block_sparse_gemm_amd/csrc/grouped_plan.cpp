@@ -33,8 +33,21 @@ static int tile_rows(int64_t M, int E, int K, int N, int epi, int dtype, int ncu
 // workgroups a compute unit; narrower tiles where wide ones are few.
 // Measured, 128 / 256 rows a tile: 64 experts of 256 rows 53 / 62 us, of 2048
 // rows 1099 / 1071 us.
-GroupedPlan grouped_wgrad_plan(int64_t M, int K, int N, int E, int dtype, int ncu) {
+//
+// Segments of a group's rows where even narrow tiles are fewer than a third of
+// what two workgroups a unit take, of 256 rows or more, while the segments'
+// sums (fp32, written and read once) stay below half the operands' bytes.
+GroupedPlan grouped_wgrad_plan(int64_t M, int K, int N, int E, int dtype, int ncu,
+                               int64_t max_segments) {
     const int64_t tn = (N + 255) / 256, few = dtype == kF32 ? 2 * (int64_t)ncu : ncu;
+    const int64_t narrow = E * (((int64_t)K + 127) / 128) * ((N + 127) / 128);
+    if (3 * narrow <= 2 * (int64_t)ncu) {
+        const int64_t operands = M * ((int64_t)K + N) * elt(dtype);
+        const int64_t share = (int64_t)E * K * N * 8;
+        const int64_t n = std::min({2 * (int64_t)ncu / narrow, M / E / 256, operands / (2 * share),
+                                    max_segments, (int64_t)kMaxSegments});
+        if (n >= 2) return {128, 128, (int)n};
+    }
     if (N <= 128 || E * (((int64_t)K + 127) / 128) * tn < few) return {128, 128, 1};
     return {M / E <= 512 || E * (((int64_t)K + 255) / 256) * tn < few ? 128 : 256, 256, 1};
 }

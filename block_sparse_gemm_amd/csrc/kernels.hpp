@@ -167,6 +167,7 @@ struct GroupedParams {
     void* c;               // [M, N] (SILU_MUL_BWD: two planes)  [[E] K x N]
     void* aux_out;
     float* ws;             // sums of K segments (nseg > 1): [nseg][M][N], with b2 [nseg][2][M][N]
+                           //                               [[nseg][E][K][N]]
     int nseg;              // K segments
     int tile_rows;         // 128 or 256
     int tile_cols;         // 256, or 128 (with 128 rows, unsplit)
@@ -185,7 +186,8 @@ struct GroupedPlan {
 };
 GroupedPlan grouped_plan(int64_t M, int K, int N, int E, int epi, int dtype, int ncu,
                          int64_t max_segments);
-GroupedPlan grouped_wgrad_plan(int64_t M, int K, int N, int E, int dtype, int ncu);
+GroupedPlan grouped_wgrad_plan(int64_t M, int K, int N, int E, int dtype, int ncu,
+                               int64_t max_segments);
 
 hipError_t launch_grouped_gemm(const GroupedParams& p, int trans_b, int epi, int c_dtype, int dtype,
                                hipStream_t stream);

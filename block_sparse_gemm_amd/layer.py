@@ -122,6 +122,7 @@ class Layer:
                     bsg.grouped_gemm_workspace_bytes(A, s.f, s.d, s.E)]
             if s.backward:
                 need.append(bsg.grouped_gemm_workspace_bytes(A, s.d, s.f, s.E, epi + "_bwd"))
+                need.append(bsg.grouped_wgrad_workspace_bytes(A, s.d, s.f, s.E))
             self.ragged_ws = torch.empty(max(need), dtype=torch.uint8, device=dev) \
                 if max(need) else None
         else:
@@ -290,10 +291,13 @@ class Layer:
           workspace=ws)
         c("unpermute_combine_bwd", bsg.unpermute_combine, self.dxp, self.dest_row, None, s.T,
           s.k, s.d, self.dx)
-        c("grouped_dw2", bsg.grouped_wgrad, self.act, self.dyp, off, self.down_by_expert(self.dW2))
-        c("grouped_dw1", bsg.grouped_wgrad, self.xp, dh[0], off, self.up_by_expert(self.dW1))
+        c("grouped_dw2", bsg.grouped_wgrad, self.act, self.dyp, off, self.down_by_expert(self.dW2),
+          workspace=ws)
+        c("grouped_dw1", bsg.grouped_wgrad, self.xp, dh[0], off, self.up_by_expert(self.dW1),
+          workspace=ws)
         if sw:
-            c("grouped_dw3", bsg.grouped_wgrad, self.xp, dh[1], off, self.up_by_expert(self.dW3))
+            c("grouped_dw3", bsg.grouped_wgrad, self.xp, dh[1], off, self.up_by_expert(self.dW3),
+              workspace=ws)
         return self.grads()
 
     def clip_grads(self, max_norm, more=()):

@@ -543,6 +543,10 @@ bsg_status bsg_grouped_gemm(const void* a, const void* a2, int64_t lda, const fl
                             int64_t ldc, int c_dtype, void* aux_out, int dtype, void* workspace,
                             size_t workspace_bytes, bsg_stream_t stream);
 
+/* Bytes of a workspace that lets bsg_grouped_wgrad split long groups along
+ * their rows (0 when that product is never split, or on invalid sizes). */
+size_t bsg_grouped_wgrad_workspace_bytes(int64_t M, int K, int N, int E);
+
 /*
  * grouped_wgrad - gradient of grouped_gemm's weights (what dstd is to the
  * padded products):
@@ -552,11 +556,14 @@ bsg_status bsg_grouped_gemm(const void* a, const void* a2, int64_t lda, const fl
  *   For weights held as trans_b = 1 takes them, exchange a and dmat.
  * Groups without rows are written as zeros.  K and N must be positive
  * multiples of 8 (bf16) or 4 (fp32).  Sums in fp32.  Deterministic.
+ * workspace (optional, NULL for none; 16-byte aligned): as in
+ * bsg_grouped_gemm, here for few and small matrices over long groups, whose
+ * rows are split over workgroups.
  */
 bsg_status bsg_grouped_wgrad(const void* a, int64_t lda, const void* dmat, int64_t ldd,
                              const int32_t* row_offsets, int E, int64_t M, int K, int N, void* c,
                              int64_t ldc, int64_t stride_c, int c_dtype, int dtype,
-                             bsg_stream_t stream);
+                             void* workspace, size_t workspace_bytes, bsg_stream_t stream);
 
 /* Bytes of bsg_grad_norm's workspace. */
 size_t bsg_grad_norm_workspace_bytes(void);

@@ -100,8 +100,13 @@ int main() {
                             EXPECT(p.rows == 128 || p.rows == 256);
                             EXPECT(p.cols == 256 || (p.cols == 128 && p.rows == 128 && seg == 1));
                             EXPECT(bsg::grouped_plan(M, K, N, E, epi, dt, 256, 1).segments == 1);
-                            const bsg::GroupedPlan w = bsg::grouped_wgrad_plan(M, K, N, E, dt, 256);
+                            const bsg::GroupedPlan w = bsg::grouped_wgrad_plan(M, K, N, E, dt, 256, bsg::kMaxSegments);
                             EXPECT((w.rows == 128 || w.rows == 256) && (w.cols == 256 || w.rows == 128));
+                            EXPECT(w.segments >= 1 && w.segments <= bsg::kMaxSegments);
+                            if (w.segments > 1 && dt != BSG_E4M3)
+                                EXPECT(bsg_grouped_wgrad_workspace_bytes(M, K, N, E) / ((size_t)K * N * 4) / E >=
+                                       (size_t)w.segments);
+                            EXPECT(bsg::grouped_wgrad_plan(M, K, N, E, dt, 256, 1).segments == 1);
                             // the size query allows every plan
                             if (seg > 1) EXPECT(ws / ((size_t)M * N * 4) >= (size_t)seg);
                         }
@@ -130,13 +135,13 @@ int main() {
                                 nullptr, P, 128, BSG_BF16, nullptr, BSG_BF16, nullptr, 0, nullptr) == BSG_EINVAL);
         EXPECT(bsg_grouped_gemm(P, nullptr, 64, nullptr, P, nullptr, 128, bad, nullptr, 0, ip, 4, 10, 64, 128, 0,
                                 nullptr, P, 128, BSG_BF16, nullptr, BSG_BF16, nullptr, 0, nullptr) == BSG_EINVAL);
-        EXPECT(bsg_grouped_wgrad(P, 64, P, 128, ip, 4, 10, 64, 128, P, bad, 8192, BSG_BF16, BSG_BF16, nullptr) ==
-               BSG_EINVAL);
-        EXPECT(bsg_grouped_wgrad(P, 64, P, 128, ip, 4, bad, 64, 128, P, 128, 8192, BSG_BF16, BSG_BF16, nullptr) ==
-               BSG_EINVAL);
+        EXPECT(bsg_grouped_wgrad(P, 64, P, 128, ip, 4, 10, 64, 128, P, bad, 8192, BSG_BF16, BSG_BF16, P, 64,
+                                 nullptr) == BSG_EINVAL);
+        EXPECT(bsg_grouped_wgrad(P, 64, P, 128, ip, 4, bad, 64, 128, P, 128, 8192, BSG_BF16, BSG_BF16, P, 64,
+                                 nullptr) == BSG_EINVAL);
     }
     EXPECT(bsg_grouped_wgrad(P, 64, P, 128, ip, 1024, INT_MAX, 64, 128, P, 128, 8192, BSG_F32, BSG_BF16,
-                             nullptr) == BSG_OK);
+                             P, SIZE_MAX, nullptr) == BSG_OK);
 
     // ---- clipping: lists of every length, and the overlap check
     for (int n : {0, 1, 2, 97, 5000}) {

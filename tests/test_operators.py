@@ -267,14 +267,14 @@ SIZES = {
 SHAPES = [(64, 256), (8, 8), (24, 136), (72, 264), (520, 1000), (2048, 128)]
 
 
-@pytest.mark.parametrize("dtype", [BF16, F32, E4M3])
+OPERANDS = [(BF16, False), (BF16, True), (F32, False), (F32, True), (E4M3, True)]
+
+
+@pytest.mark.parametrize("dtype, trans", OPERANDS)
 @pytest.mark.parametrize("sizes", list(SIZES))
 @pytest.mark.parametrize("K, N", SHAPES)
-@pytest.mark.parametrize("trans", [False, True])
 def test_grouped_gemm(dtype, sizes, K, N, trans):
     if dtype == E4M3:
-        if not trans:
-            pytest.skip("e4m3 weights are K-contiguous")
         K = -(-K // 16) * 16
     sizes = SIZES[sizes]
     g = gen(K * N + len(sizes))
@@ -337,16 +337,18 @@ def acts_exact(epi, p, q, aux):
     return [p * aux[1], p * aux[0]], [(aux[1].abs(), 0), (aux[0].abs(), 0)]
 
 
-@pytest.mark.parametrize("dtype", [BF16, F32, E4M3])
+# e4m3 has forward products only, and the backward ones save nothing
+EPILOGUES = [(dt, tr, epi, save) for dt, tr in OPERANDS
+             for epi in ("gelu", "silu_mul", "gelu_bwd", "silu_mul_bwd") for save in (False, True)
+             if not (save and epi.endswith("bwd")) and
+             not (dt == E4M3 and (save or epi.endswith("bwd")))]
+
+
+@pytest.mark.parametrize("dtype, trans, epi, save", EPILOGUES)
 @pytest.mark.parametrize("sizes", ["tile edges", "few"])
 @pytest.mark.parametrize("K, N", [(64, 264), (200, 136), (1032, 512)])
-@pytest.mark.parametrize("trans", [False, True])
-@pytest.mark.parametrize("epi", ["gelu", "silu_mul", "gelu_bwd", "silu_mul_bwd"])
-@pytest.mark.parametrize("save", [False, True])
 def test_grouped_gemm_epilogues(dtype, sizes, K, N, trans, epi, save):
     bwd = epi.endswith("bwd")
-    if (bwd and save) or (dtype == E4M3 and (bwd or save or not trans)):
-        pytest.skip("no such product")
     if dtype == E4M3:
         K = -(-K // 16) * 16
     sizes = SIZES[sizes]
@@ -547,6 +549,37 @@ def test_grouped_wgrad(dtype, sizes, K, N, side):
     f.fill_(9.0)
     bsg.grouped_wgrad(a[:0], d[:0], torch.zeros_like(off), f)
     assert bool((f == 0).all())
+
+
+@pytest.mark.parametrize("dtype, out", [(BF16, BF16), (BF16, F32), (F32, F32)])
+@pytest.mark.parametrize("sizes, K, N", [([5000], 136, 72), ([0, 2100, 3, 1300], 64, 264),
+                                         ([1500, 1600], 256, 128)])
+def test_grouped_wgrad_split_along_rows(dtype, out, sizes, K, N):
+    """Few small matrices over long groups: every number of segments."""
+    g = gen(6)
+    E, M = len(sizes), sum(sizes)
+    off = offsets(sizes)
+    a, d = randn(g, M, K, dtype=dtype), randn(g, M, N, dtype=dtype)
+    share = E * K * N
+    most = bsg.grouped_wgrad_workspace_bytes(M, K, N, E) // 4
+    assert most >= 2 * share
+    o = off.tolist()
+    for floats in (0, share, 2 * share, most):
+        ws = torch.full((floats + 64,), 7.0, device="cuda")
+        got = []
+        for _ in range(2):
+            big = torch.full((K, E * N + 8), 9.0, device="cuda", dtype=out)
+            c = big[:, :E * N].unflatten(1, (E, N)).permute(1, 0, 2)
+            bsg.grouped_wgrad(a, d, off, c, workspace=ws[:floats] if floats else None)
+            got.append(big)
+        assert torch.equal(got[0], got[1]) and bool((ws[floats:] == 7).all())
+        assert bool((big[:, E * N:] == 9).all())
+        for e in range(E):
+            r = slice(o[e], o[e + 1])
+            ad, dd = a[r].double().t().contiguous(), d[r].double()
+            want, s = ad @ dd, ad.abs() @ dd.abs()
+            close(f"expert {e}, {floats} floats", c[e], want,
+                  u(out) * want.abs() + e_sum(sizes[e], s))
 
 
 # --------------------------------------------------------------- clipping

@@ -109,12 +109,13 @@ def test_grouped_gemm_refusals(L, over, want):
 
 
 def test_grouped_wgrad_refusals(L):
-    call = caller(L.bsg_grouped_wgrad, "a lda d ldd off E M K N c ldc sc cdt dt s".split(),
-                  [P, 64, P, 128, P, 4, 100, 64, 128, P, 128, 8192, bsg.BF16, bsg.BF16, None])
+    call = caller(L.bsg_grouped_wgrad, "a lda d ldd off E M K N c ldc sc cdt dt ws wsb s".split(),
+                  [P, 64, P, 128, P, 4, 100, 64, 128, P, 128, 8192, bsg.BF16, bsg.BF16, None, 0,
+                   None])
     for over in (dict(a=None), dict(d=MIS), dict(off=None), dict(c=None), dict(E=0), dict(E=1025),
                  dict(M=-1), dict(K=4), dict(N=4), dict(K=72), dict(N=136), dict(lda=68),
                  dict(ldd=132), dict(ldc=64), dict(ldc=132), dict(sc=0), dict(sc=4),
-                 dict(dt=bsg.E4M3), dict(cdt=3)):
+                 dict(dt=bsg.E4M3), dict(cdt=3), dict(ws=MIS, wsb=64)):
         assert call(**over) == bsg.EINVAL, over
     assert call(dt=bsg.F32) == bsg.EUNSUPPORTED
     assert call(lda=1 << 27) == bsg.EUNSUPPORTED
