@@ -6,15 +6,26 @@
 //                   of expert e, row_offsets[e] <= r < row_offsets[e + 1]
 //   grouped_wgrad   C_e[k][n] = sum over those rows r of A[r][k] D[r][n]
 //
-// This file: the tile kernel, for groups of many rows and for weight
-// gradients.  A workgroup of four waves computes a 256 x 256 output tile as
-// four 128 x 128 quadrants of 4 x 4 v_mfma_f32_32x32x16_bf16 accumulators
-// (v_mfma_f32_32x32x2_f32 for fp32, v_mfma_f32_32x32x64_f8f6f4 for e4m3); a
-// group's last rows, when at most 128, run as a tile of half the height.
+// One tile body serves them all.  A workgroup of four waves computes an output
+// tile of 256 x 256 as four 128 x 128 quadrants of 4 x 4
+// v_mfma_f32_32x32x16_bf16 accumulators (v_mfma_f32_32x32x2_f32 for fp32,
+// v_mfma_f32_32x32x64_f8f6f4 for e4m3), a group's last rows, when at most 128,
+// as a tile of half the height; or tiles of 128 x 256 or 128 x 128, two
+// workgroups a compute unit (grouped_plan.cpp says which and why).
+//
+// Measured, us: dense 8192^3, one expert, bf16 823 (1336 TFLOP/s), e4m3 424
+// (2596); e4m3 SwiGLU prompt, 8 experts of 2048 rows, K 4096, N 14336, 1684
+// (2290 TFLOP/s); one token of two such experts in bf16 84 (5.6 TB/s of
+// weights); 64 experts of 256 rows, K 512, N 2048, GeLU with its derivative,
+// 64; weight gradients, 8 experts of 2048 rows, 4096 x 14336, 1600 (1200
+// TFLOP/s).  The long loops are bound by the direct loads' address unit (busy
+// 96 % of the cycles with both operands K-contiguous, where a row piece is 64
+// bytes) and by the power that the matrix cores may draw, the e4m3 products
+// also by their epilogues, the few-row products by HBM.
 //
 // Operand panels of 128 rows x 64 bytes of K go from memory to LDS with
-// buffer_load_dwordx4 ... lds through a ring of four stages.  The buffer
-// descriptor of each panel ends where its data ends: rows past the group,
+// buffer_load_dwordx4 ... lds through a ring of stages.  The buffer
+// descriptor of each operand ends where its data ends: rows past the group,
 // columns past the matrix and the K positions behind the last one are out of
 // the descriptor's range, which the hardware reads as zero.  So no load of
 // another expert's rows reaches an accumulator that is stored, no padding is
@@ -632,9 +643,18 @@ __device__ __forceinline__ void ragged_tile(char* smem, const Operand (*op)[3], 
 // ----------------------------------------------------------------- kernels
 
 // Row tiles of one group taken together, down the rows first (see
-// grouped_tile in common.hpp): the tiles that run at once on one XCD share
-// both operands' panels.
-constexpr int kGroupedRows = 8;
+// grouped_tile in common.hpp), and kGroupedChunk consecutive tiles, one for
+// each compute unit of an XCD, dealt to the XCDs in turn: what an XCD runs at
+// once is 4 x 8 tiles that share both operands' panels in its L2, and the chip
+// works on one region of the output.  Against a contiguous eighth of all tiles
+// for each XCD, with 8 rows together, us: 8 experts of 2048 rows, K 14336,
+// N 4096: 1827 -> 1661; e4m3 SwiGLU, K 4096, N 14336: 1752 -> 1684; 64 skewed
+// experts, K 4096, N 1024: 1085 -> 1041; K 1024, N 4096: 1214 -> 1248.  Groups
+// of a few rows read each weight once in either order, and fastest from
+// contiguous ranges: 8 experts of 12 rows, K 4096, e4m3 196 against 203.
+constexpr int kGroupedRows = 4;
+constexpr int kGroupedChunk = 32;
+constexpr int kChunkedRows = 64;  // rows a group on average from which chunks are dealt
 
 // H x W: rows and columns of a tile (DUAL: W = 256, of which each product has
 // 128).  256 rows: one workgroup a compute unit, a group's last rows (at most
@@ -659,8 +679,9 @@ __global__ __launch_bounds__(kGemmThreads, (TileShape<H, W>::kPerCu)) void group
     const int ntiles = groups.count() * tn;
     const int nseg = SPLIT ? P.nseg : 1;
     if ((int)blockIdx.x >= ntiles * nseg) return;
-    // segment-major: what an XCD runs at once shares one K segment of its operands
-    const int v = xcd_remap(blockIdx.x, ntiles * nseg);
+    // split: segment-major, so that what an XCD runs at once shares one K segment
+    const bool dealt = !SPLIT && P.M >= (int64_t)kChunkedRows * P.E;
+    const int v = dealt ? xcd_chunked(blockIdx.x, ntiles, kGroupedChunk) : xcd_remap(blockIdx.x, ntiles * nseg);
     const int seg = SPLIT ? v / ntiles : 0;
     const Group g = groups.find(v - seg * ntiles, tn);
     int tm, tq;
