@@ -342,7 +342,9 @@ class Norm:
     buffers: ``forward`` adds the residual stream (h = x + residual) and
     normalises the sum, in x's type or, with ``e4m3``, in 8 bits with one
     scale a row; ``backward`` gives the gradient of both addends and of the
-    weight."""
+    weight.  A Norm with a residual's buffer takes calls without one too (a
+    model's first norm); its backward reads what the last forward normalised,
+    x itself then."""
 
     def __init__(self, T: int, d: int, weight: torch.Tensor, eps: float = 1e-5, residual=True,
                  e4m3=False, backward=False):
@@ -359,9 +361,11 @@ class Norm:
                                   device=dev)
 
     def forward(self, x, residual=None):
-        bsg.rms_norm(x, self.weight, self.eps, self.y, h=self.h, residual=residual,
-                     y_scale=self.y_scale, rstd=self.rstd)
+        if residual is not None and self.h is None:
+            raise ValueError("Norm: made without a residual")
         self.stored = x if residual is None else self.h
+        bsg.rms_norm(x, self.weight, self.eps, self.y, h=None if residual is None else self.h,
+                     residual=residual, y_scale=self.y_scale, rstd=self.rstd)
         return self.y
 
     def backward(self, dy, dh=None):

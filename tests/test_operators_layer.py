@@ -365,3 +365,16 @@ def test_refusals_of_tensors_that_do_not_agree():
     with pytest.raises(bsg.BsgError) as e:  # the norm's tensors twice in place
         bsg.grad_clip([s4, s4], torch.zeros((), device="cuda"), 1.0)
     assert e.value.status == bsg.EINVAL
+
+
+def test_norm_with_and_without_a_residual():
+    g = gen(5)
+    x, r, dy = (randn(g, 9, 72) for _ in range(3))
+    w = randn(g, 72)
+    both, plain = layer.Norm(9, 72, w, backward=True), layer.Norm(9, 72, w, residual=False,
+                                                                  backward=True)
+    both.forward(r, x)
+    assert torch.equal(both.forward(x), plain.forward(x))
+    assert all(torch.equal(a, b) for a, b in zip(both.backward(dy), plain.backward(dy)))
+    with pytest.raises(ValueError):  # nowhere to keep the sum that the backward needs
+        plain.forward(x, r)
