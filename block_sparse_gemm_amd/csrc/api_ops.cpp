@@ -375,8 +375,9 @@ bsg_status bsg_grad_clip(void* const* grads, void* const* out, const int64_t* co
     if (s != BSG_OK) return s;
     REQUIRE_PTR(norm);
     REQUIRE(max_norm >= 0.0f, "max_norm must be >= 0");
-    // what is written overlaps nothing else: ranges sorted by address, an
-    // input that is its own output counted once
+    // what is written overlaps nothing else, the norm included, which every
+    // workgroup reads: ranges sorted by address, an input that is its own
+    // output counted once
     struct Range {
         uintptr_t lo, hi;
         bool written;
@@ -384,6 +385,7 @@ bsg_status bsg_grad_clip(void* const* grads, void* const* out, const int64_t* co
     Range* r = new (std::nothrow) Range[2 * (size_t)n + 1];
     REQUIRE(r != nullptr, "out of host memory");
     size_t m = 0;
+    r[m++] = Range{(uintptr_t)norm, (uintptr_t)norm + sizeof(float), false};
     for (int i = 0; i < n; ++i) {
         if (counts[i] == 0) continue;
         const uintptr_t bytes = (uintptr_t)counts[i] * elt_bytes(dtypes[i]);
@@ -400,7 +402,7 @@ bsg_status bsg_grad_clip(void* const* grads, void* const* out, const int64_t* co
         if (r[i].written) written_end = std::max(written_end, r[i].hi);
     }
     delete[] r;
-    REQUIRE(apart, "a tensor that is written overlaps another one of the call");
+    REQUIRE(apart, "a tensor that is written overlaps the norm or another one of the call");
     return hip_status(bsg::launch_grad_clip(grads, out, counts, dtypes, n, norm, max_norm,
                                             (hipStream_t)stream),
                       "grad_clip");

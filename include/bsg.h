@@ -591,7 +591,8 @@ bsg_status bsg_grad_norm(const void* const* grads, const int64_t* counts, const 
  *   grads, counts, dtypes as bsg_grad_norm; out: a HOST array of n device
  *   pointers to results of the same sizes and types, or NULL for in place.
  *   out[i] is grads[i] or overlaps no tensor of the call; in place, the
- *   tensors do not overlap each other (else BSG_EINVAL).  max_norm >= 0.
+ *   tensors do not overlap each other; norm lies in no tensor that is written
+ *   (else BSG_EINVAL).  max_norm >= 0.
  */
 bsg_status bsg_grad_clip(void* const* grads, void* const* out, const int64_t* counts,
                          const int* dtypes, int n, const float* norm, float max_norm,

@@ -184,3 +184,10 @@ def test_binding_refuses_what_is_not_on_the_gpu():
         bsg.grouped_gemm(x, torch.zeros(2, dtype=torch.int32), x.view(1, 64, 4), x)
     with pytest.raises(ValueError, match="current GPU"):
         bsg.grad_norm([x], torch.zeros(1), x)
+
+
+def test_grad_clip_refuses_a_norm_that_it_would_write(L):
+    a, b, c, n = _list((0x1000, 0x2000), (5, 7), (bsg.F32, bsg.F32))
+    o = (C.c_void_p * n)(0x3000, 0x4000)
+    for out, norm in ((None, 0x1000), (None, 0x1010), (None, 0x2018), (o, 0x3000), (o, 0x4008)):
+        assert L.bsg_grad_clip(a, out, b, c, n, norm, 1.0, None) == bsg.EINVAL
