@@ -684,6 +684,8 @@ __global__ __launch_bounds__(kGemmThreads, (TileShape<H, W>::kPerCu)) void group
     const int v = dealt ? xcd_chunked(blockIdx.x, ntiles, kGroupedChunk) : xcd_remap(blockIdx.x, ntiles * nseg);
     const int seg = SPLIT ? v / ntiles : 0;
     const Group g = groups.find(v - seg * ntiles, tn);
+    // offsets that do not ascend may add up to more tiles than an int holds
+    if ((unsigned)g.local >= (unsigned)((g.rows + H - 1) / H * tn)) return;
     int tm, tq;
     grouped_tile(g.local, (g.rows + H - 1) / H, tn, kGroupedRows, tm, tq);
     const int mr = min(H, g.rows - H * tm);
