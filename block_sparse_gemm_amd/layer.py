@@ -145,8 +145,10 @@ class Layer:
         self.gp = torch.zeros(kept, dtype=dt, device=dev) if s.backward else None
         self.yp = torch.zeros(self.Tp_max, s.d, dtype=ydt, device=dev)
         self.y = torch.zeros(s.T, s.d, dtype=dt, device=dev)
-        self.clip_ws = self.grad_norm = None
         if s.backward:
+            self.clip_ws = torch.empty(bsg.grad_norm_workspace_bytes(), dtype=torch.uint8,
+                                       device=dev)
+            self.grad_norm = torch.zeros((), dtype=torch.float32, device=dev)
             self.dyp = torch.zeros(self.Tp_max, s.d, dtype=dt, device=dev)
             self.row_src_b = torch.zeros(self.Tp_max, **i32)
             # SwiGLU: plane 0 the gate projection's gradient, plane 1 the up's
@@ -305,11 +307,6 @@ class Layer:
         (a router's, a norm's), in place to a joint 2-norm of at most
         max_norm; returns the norm before (one fp32 on the device)."""
         grads = [*self.grads()[1:], *more]
-        if self.clip_ws is None:
-            dev = self.dW1.device
-            self.clip_ws = torch.empty(bsg.grad_norm_workspace_bytes(), dtype=torch.uint8,
-                                       device=dev)
-            self.grad_norm = torch.zeros((), dtype=torch.float32, device=dev)
         self._call("grad_norm", bsg.grad_norm, grads, self.grad_norm, self.clip_ws)
         self._call("grad_clip", bsg.grad_clip, grads, self.grad_norm, max_norm)
         return self.grad_norm
@@ -328,10 +325,13 @@ class Layer:
     # ---------------------------------------------------------- helpers
     def sparse_rows(self, blocks: torch.Tensor, rows: torch.Tensor) -> torch.Tensor:
         """Gather full rows [len(rows), f] of a block-major sparse operand
-        (host-side inspection helper; rows are padded-row indices)."""
+        (host-side inspection helper; rows are padded-row indices), or of a
+        ragged layer's matrix."""
+        r = rows.long()
+        if self.ragged:
+            return blocks[r]
         F, br = self.topo.F, self.block_rows
         b = blocks.view(-1, br, bsg.BLOCK)
-        r = rows.long()
         base = (r // br) * F
         out = [b[base + j, r % br] for j in range(F)]
         return torch.cat(out, dim=1)

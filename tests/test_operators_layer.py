@@ -378,3 +378,12 @@ def test_norm_with_and_without_a_residual():
     assert all(torch.equal(a, b) for a, b in zip(both.backward(dy), plain.backward(dy)))
     with pytest.raises(ValueError):  # nowhere to keep the sum that the backward needs
         plain.forward(x, r)
+
+
+def test_ragged_layer_rows_and_clipping_buffers():
+    s = layer.Shape(T=16, d=64, E=4, f=72, k=2, dtype="f32", bin_rows=1, backward=True)
+    m = layer.Layer(s)
+    m.act.normal_()
+    rows = torch.tensor([3, 0, 31], device="cuda", dtype=torch.int32)
+    assert torch.equal(m.sparse_rows(m.act, rows), m.act[[3, 0, 31]])
+    assert m.grad_norm.numel() == 1 and m.clip_ws.numel() == bsg.grad_norm_workspace_bytes()
