@@ -381,8 +381,8 @@ def _address(t):
 
 def _rows(call, name, t, shape, dtype):
     """The leading dimension of a row-major [T, d] tensor."""
-    if t.shape != shape or t.dtype != dtype:
-        _fail(call, f"{name} must be a {list(shape)} tensor of {dtype}")
+    if t.shape != shape or t.dtype != dtype or shape[1] >> 31:
+        _fail(call, f"{name} must be a {list(shape)} tensor of {dtype}, under 2^31 wide")
     ld, one = t.stride()
     if one != 1 and shape[1] > 1 and shape[0]:
         _fail(call, f"{name} must be row-major")
@@ -459,8 +459,8 @@ def _operand_code(t):
 
 def _matrices(call, name, t, shape, dtype):
     """(ld, stride) of one matrix an expert, [E, rows, cols] with contiguous rows."""
-    if t.shape != shape or t.dtype != dtype:
-        _fail(call, f"{name} must be a {list(shape)} tensor of {dtype}")
+    if t.shape != shape or t.dtype != dtype or max(shape) >> 31:
+        _fail(call, f"{name} must be a {list(shape)} tensor of {dtype}, sizes under 2^31")
     stride, ld, one = t.stride()
     if one != 1 and shape[2] > 1:
         _fail(call, f"{name} must have contiguous rows")

@@ -458,8 +458,9 @@ bsg_status bsg_unpermute_combine(const void* yp, int yp_dtype, int64_t ld_yp,
  * d must be a positive multiple of 8 (bf16) or 4 (fp32), rows of at most 32
  * KiB (else BSG_EUNSUPPORTED); rows of every array 16-byte aligned, rows of
  * an e4m3 y 8-byte (bf16 x) or 4-byte (fp32 x) aligned.  eps finite, >= 0.
- * h may be x or residual and y may be x (in place, same leading dimension);
- * otherwise inputs and outputs do not overlap.  T = 0 does nothing.
+ * h may be x or residual and a y of their type may be x (in place, same
+ * leading dimension); otherwise inputs and outputs do not overlap.  T = 0 does
+ * nothing.
  */
 bsg_status bsg_rms_norm(const void* x, int64_t ldx, const void* residual, int64_t ldr,
                         const void* weight, float eps, int64_t T, int d, int dtype, void* h,

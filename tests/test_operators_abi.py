@@ -191,3 +191,16 @@ def test_grad_clip_refuses_a_norm_that_it_would_write(L):
     o = (C.c_void_p * n)(0x3000, 0x4000)
     for out, norm in ((None, 0x1000), (None, 0x1010), (None, 0x2018), (o, 0x3000), (o, 0x4008)):
         assert L.bsg_grad_clip(a, out, b, c, n, norm, 1.0, None) == bsg.EINVAL
+
+
+def test_binding_refuses_sizes_beyond_the_c_types():
+    def empty(*shape):
+        return torch.empty(shape, dtype=torch.bfloat16, device="meta")
+
+    wide = empty(2, (1 << 32) + 64)
+    with pytest.raises(ValueError):
+        bsg._rows("rms_norm", "x", wide, wide.shape, wide.dtype)
+    for shape in ((1, 8, (1 << 32) + 64), (1, (1 << 32) + 64, 8), ((1 << 32) + 1, 1, 8)):
+        b = empty(*shape)
+        with pytest.raises(ValueError):
+            bsg._matrices("grouped_gemm", "b", b, b.shape, b.dtype)
