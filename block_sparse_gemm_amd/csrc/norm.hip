@@ -16,10 +16,11 @@
 // between its reductions, so everything is read once and written once: a
 // wave owns a row where it holds it in few registers, several waves a wider
 // one.  The weight row is loaded once per wave and kept over its rows, and the
-// next rows' loads are in flight while a row is worked on.  Measured (rotating inputs larger than the caches): forward with the
-// residual, 8192 x 4096 bf16 49 us (5.4 TB/s; a large copy reaches 5.7), to
-// e4m3 46 us, 65536 x 1024 103 us, four rows of 4096 3.4 us; backward with the
-// residual's gradient, 65536 x 1024 102 us (5.3 TB/s), 8192 x 4096 55 us.
+// next rows' loads are in flight while a row is worked on.  Measured
+// (rotating inputs larger than the caches): forward with the residual, 8192 x
+// 4096 bf16 49 us (5.4 TB/s; a large copy reaches 5.7), to e4m3 46 us, 65536 x
+// 1024 103 us, four rows of 4096 3.4 us; backward with the residual's
+// gradient, 65536 x 1024 102 us (5.3 TB/s), 8192 x 4096 55 us.
 #include "common.hpp"
 #include "kernels.hpp"
 
@@ -399,6 +400,11 @@ hipError_t bwd_go(const NormParams& p, int grid, hipStream_t s) {
 template <int DT>
 hipError_t bwd_pick(const NormParams& p, int grid, hipStream_t s) {
     const int vecs = p.d / Vec<DT>::kN;
+    // three rows of values and the next three stay in registers, so a wave
+    // holds at most 2 vectors a lane of each (4 in the widest rows only) and wider
+    // rows take more threads; 2 vectors a thread from 4 waves on: 8192 x 4096 bf16, 256 threads of 2 / 512
+    // of 1, 55.3 / 57.9 us.  Loads ahead / not: 65536 x 1024 102 / 107 us, 16384 x
+    // 512 15.7 / 19.4.
     if (vecs <= 64) return bwd_go<DT, 64, 1>(p, grid, s);
     if (vecs <= 128) return bwd_go<DT, 64, 2>(p, grid, s);
     if (vecs <= 256) return bwd_go<DT, 256, 1>(p, grid, s);
