@@ -675,3 +675,79 @@ def test_same_bits_on_every_run():
     for dw in dws:
         bsg.rms_norm_backward(dy, h, w, rstd, torch.empty_like(h), dw, ws)
     assert torch.equal(dws[0], dws[1]) and torch.equal(dws[0], dws[2])
+
+
+# ------------------------------------------- many tiles, offsets past 32 bits
+
+@pytest.mark.parametrize("dtype, trans", OPERANDS)
+@pytest.mark.parametrize("K, most", [(96, 2), (1040, 1)])
+def test_grouped_gemm_over_many_tiles(dtype, trans, K, most):
+    """Several hundred tiles of uneven groups.  Small integers: every sum is
+    below 2^24 and so exact in any order (8-bit: no product below 2^-13 of
+    another but 0), and the result is its one rounding."""
+    E, N = 37, 1304
+    sizes = [(i * 61) % 401 for i in range(E)]
+    M = sum(sizes) + 50
+    g = gen(K)
+    a = torch.randint(-most, most + 1, (M, K), generator=g, device="cuda").float().to(dtype)
+    b = torch.randint(-most, most + 1, (E, N, K) if trans else (E, K, N), generator=g,
+                      device="cuda").float().to(dtype)
+    off = offsets(sizes)
+    out = F32 if dtype == F32 else BF16
+    c = torch.full((M, N), 9.0, device="cuda", dtype=out)
+    scales = dict(a_scale=torch.ones(M, device="cuda"),
+                  b_scale=torch.ones(E, N, device="cuda")) if dtype == E4M3 else {}
+    bsg.grouped_gemm(a, off, b, c, trans_b=trans, **scales)
+    want = products_exact(a, b, off, trans)[0]
+    assert torch.equal(c[:-50], want[:-50].to(out)) and bool((c[-50:] == 9).all())
+
+
+def test_rows_past_4_gib():
+    """Rows so far apart that their byte offsets pass 2^32: the same bits as
+    from rows side by side."""
+    M, K, N, ld = 33000, 64, 72, 65544
+    g = gen(7)
+    a, d, r = randn(g, M, K, dtype=BF16), randn(g, M, N, dtype=BF16), randn(g, M, K, dtype=BF16)
+    b = randn(g, 4, K, N, dtype=BF16)
+    off = offsets([20000, 0, 12990, 10])
+
+    def apart(t):
+        v = torch.empty(M, ld, device="cuda", dtype=t.dtype)[:, :t.shape[1]]
+        v.copy_(t)
+        return v
+
+    A, D, R = apart(a), apart(d), apart(r)
+    c, C = torch.empty(M, N, device="cuda", dtype=BF16), apart(d)
+    bsg.grouped_gemm(a, off, b, c)
+    bsg.grouped_gemm(A, off, b, C)
+    assert torch.equal(c, C)
+    w, W = (torch.empty(4, K, N, device="cuda", dtype=BF16) for _ in range(2))
+    bsg.grouped_wgrad(a, d, off, w)
+    bsg.grouped_wgrad(A, D, off, W)
+    assert torch.equal(w, W)
+    wn = randn(g, K, dtype=BF16)
+    y, h, s = torch.empty_like(a), torch.empty_like(a), torch.empty(M, device="cuda")
+    bsg.rms_norm(a, wn, 1e-5, y, h=h, residual=r, rstd=s)
+    bsg.rms_norm(A, wn, 1e-5, A, h=R, residual=R)
+    assert torch.equal(y, A) and torch.equal(h, R)
+    ws = torch.empty(bsg.rms_norm_backward_workspace_bytes(M, K), device="cuda", dtype=torch.uint8)
+    dx, dw, dW = torch.empty_like(a), torch.empty(K, device="cuda"), torch.empty(K, device="cuda")
+    bsg.rms_norm_backward(a, h, wn, s, dx, dw, ws)
+    A.copy_(a)
+    bsg.rms_norm_backward(A, R, wn, s, A, dW, ws)
+    assert torch.equal(dx, A) and torch.equal(dw, dW)
+
+
+def test_clipping_a_tensor_of_more_than_2_31_values():
+    n = (1 << 31) + 5
+    t = torch.full((n,), 2.0 ** -10, device="cuda", dtype=BF16)
+    t[-1] = 2.0 ** 10
+    ws = workspace()
+    norm = torch.zeros((), device="cuda")
+    bsg.grad_norm([t], norm, ws)
+    # squares and their sum are exact in fp64 (below 2^53 steps of 2^-20); one root, one rounding
+    want = float(torch.tensor((2.0 ** -20 * (n - 1) + 2.0 ** 20) ** 0.5, dtype=torch.float64).float())
+    assert float(norm) == want
+    norm.fill_(4.0)
+    bsg.grad_clip([t], norm, 2.0)
+    assert float(t[-1]) == 512.0 and bool((t[:-1] == 2.0 ** -11).all())
